@@ -7,7 +7,8 @@ if libbsg.so is missing or a call fails, a RuntimeError is raised.
 
 Entry points keep the C names:
     gemm_amax, grouped_gemm, grouped_gemm_srelu, grouped_gemm_dswiglu,
-    gemm_proj_rope_mxfp8, grouped_gemm_discrete, grouped_gemm_srelu_discrete
+    gemm_proj_rope_mxfp8, grouped_gemm_discrete, grouped_gemm_srelu_discrete,
+    quant_i8, gemm_i8, gemm_glu, gemm_glu_i8, gemm_glu_bwd
 and validate_only=True calls the host-only check bsg_validate_<name>.
 """
 from __future__ import annotations
@@ -25,6 +26,11 @@ F32, F16, BF16, E4M3, E5M2, E2M1X2, E8M0 = range(7)
 _TORCH_DT = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 STATUS = {0: "OK", 1: "NULLPTR", 2: "SHAPE", 3: "DTYPE", 4: "ALIGN", 5: "UNSUPPORTED",
           6: "DEVICE", 7: "LAUNCH"}
+
+# the feed-forward operators, bsg_act and bsg_op
+_FFN_OPS = ["quant_i8", "gemm_i8", "gemm_glu", "gemm_glu_i8", "gemm_glu_bwd"]
+_ACTS = {"silu": 0, "gelu_tanh": 1, "relu": 2}
+_WS_OPS = {"gemm_i8": 0, "gemm_glu": 1, "gemm_glu_i8": 2, "gemm_glu_bwd": 3}
 
 
 class BsgError(RuntimeError):
@@ -60,11 +66,20 @@ def lib():
             "bsg_validate_grouped_gemm_srelu": [p] * 14 + [i64] * 4 + [i32] * 4 + [f32],
             "bsg_validate_gemm_proj_rope_mxfp8": [p] * 10 + [i64] * 5 + [i32, i32],
             "bsg_check_padded_offsets": [p, i64, i64, p],
+            "quant_i8": [p] * 3 + [i64] * 2 + [i32, p],
+            "gemm_i8": [p] * 7 + [i64] * 4 + [i32, i32, p],
+            "gemm_glu": [p] * 7 + [i64] * 4 + [i32, i32, p],
+            "gemm_glu_i8": [p] * 8 + [i64] * 4 + [i32, i32, p],
+            "gemm_glu_bwd": [p] * 10 + [i64] * 4 + [i32, i32, p],
         }
+        for name in _FFN_OPS:
+            sigs["bsg_validate_" + name] = sigs[name][:-1]
         for name, args in sigs.items():
             fn = getattr(L, name)
             fn.argtypes = args
             fn.restype = i32
+        L.bsg_workspace_bytes.restype = i64
+        L.bsg_workspace_bytes.argtypes = [i32, i64, i64, i64]
         L.bsg_status_string.restype = ctypes.c_char_p
         L.bsg_status_string.argtypes = [i32]
         L.bsg_last_error.restype = ctypes.c_char_p
@@ -82,7 +97,8 @@ def symbols():
             "bsg_validate_grouped_gemm_srelu", "bsg_validate_gemm_proj_rope_mxfp8",
             "bsg_validate_grouped_gemm_dswiglu",
             "bsg_validate_grouped_gemm_discrete", "bsg_validate_grouped_gemm_srelu_discrete",
-            "bsg_check_padded_offsets", "bsg_status_string", "bsg_last_error", "bsg_version"]
+            "bsg_check_padded_offsets", "bsg_status_string", "bsg_last_error", "bsg_version",
+            *_FFN_OPS, *("bsg_validate_" + n for n in _FFN_OPS), "bsg_workspace_bytes"]
 
 
 def _ptr(t):
@@ -398,3 +414,121 @@ def gemm_proj_rope_mxfp8(x, w, x_scale, w_scale, cos, sin, out_fp8_row, out_scal
     if validate_only:
         return lib().bsg_validate_gemm_proj_rope_mxfp8(*args)
     _check(lib().gemm_proj_rope_mxfp8(*args, _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# Feed-forward operators
+# ---------------------------------------------------------------------------
+def workspace_bytes(name, m, n, k) -> int:
+    """Scratch bytes that operator `name` takes at these sizes (0 for
+    quant_i8).  A program keeps one such buffer beside its layer."""
+    if name == "quant_i8":
+        return 0
+    if name not in _WS_OPS:
+        raise ValueError(f"no operator named {name!r}")
+    b = lib().bsg_workspace_bytes(_WS_OPS[name], m, n, k)
+    if b < 0:
+        raise BsgError(2, f"{name}: sizes {(m, n, k)} are not sizes")
+    return b
+
+
+def _act(act) -> int:
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
+    return _ACTS[act]
+
+
+def _ws(workspace, name, m, n, k):
+    """(address, bytes) of a workspace; a plain address is taken to be large enough."""
+    if workspace is None:
+        return None, 0
+    if isinstance(workspace, int):
+        return workspace, lib().bsg_workspace_bytes(_WS_OPS[name], m, n, k)
+    _need(workspace, "workspace", 0)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def quant_i8(x, q, scale, m, k, x_dtype=None, stream=None, validate_only=False):
+    """Rows of x (m, k) -> 8-bit integers q and one fp32 scale a row (see
+    include/bsg.h).  x_dtype: torch.float32 / float16 / bfloat16, from x if None."""
+    xd = dtype_code(x_dtype if x_dtype is not None else x)
+    _need(x, "x", _out_bytes(xd, m * k), xd)
+    _need(q, "q", m * k, torch.int8)
+    _need(scale, "scale", 4 * m, torch.float32)
+    args = [_ptr(x), _ptr(q), _ptr(scale), m, k, xd]
+    if validate_only:
+        return lib().bsg_validate_quant_i8(*args)
+    _check(lib().quant_i8(*args, _stream(stream)))
+
+
+def gemm_i8(a, b, a_scale, b_scale, bias, c, m, n, k, bias_dtype=None, c_dtype=None, workspace=None,
+            stream=None, validate_only=False):
+    """c = (a b^T) * a_scale[:, None] * b_scale + bias from 8-bit integers
+    (see include/bsg.h).  bias may be None."""
+    cd = dtype_code(c_dtype if c_dtype is not None else c)
+    bd = dtype_code(bias_dtype if bias_dtype is not None else (bias if bias is not None else torch.float32))
+    _need(a, "a", m * k, torch.int8)
+    _need(b, "b", n * k, torch.int8)
+    _need(a_scale, "a_scale", 4 * m, torch.float32)
+    _need(b_scale, "b_scale", 4 * n, torch.float32)
+    _need(bias, "bias", _out_bytes(bd, n), bd)
+    _need(c, "c", _out_bytes(cd, m * n), cd)
+    args = [_ptr(a), _ptr(b), _ptr(a_scale), _ptr(b_scale), _ptr(bias), _ptr(c),
+            *_ws(workspace, "gemm_i8", m, n, k), m, n, k, bd, cd]
+    if validate_only:
+        return lib().bsg_validate_gemm_i8(*args)
+    _check(lib().gemm_i8(*args, _stream(stream)))
+
+
+def gemm_glu(x, w_gate, w_up, h, g, u, m, n, k, act="silu", dtype=None, workspace=None, stream=None,
+             validate_only=False):
+    """h = act(x w_gate^T) * (x w_up^T), and the two products in g and u
+    unless they are None (see include/bsg.h).  act: "silu", "gelu_tanh" or
+    "relu".  dtype: torch.float16 / bfloat16 of every tensor, from x if None."""
+    dt = dtype_code(dtype if dtype is not None else x)
+    mn = _out_bytes(dt, m * n)
+    _need(x, "x", _out_bytes(dt, m * k), dt)
+    _need(w_gate, "w_gate", _out_bytes(dt, n * k), dt)
+    _need(w_up, "w_up", _out_bytes(dt, n * k), dt)
+    _need(h, "h", mn, dt)
+    _need(g, "g", mn, dt)
+    _need(u, "u", mn, dt)
+    args = [_ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(h), _ptr(g), _ptr(u),
+            *_ws(workspace, "gemm_glu", m, n, k), m, n, k, dt, _act(act)]
+    if validate_only:
+        return lib().bsg_validate_gemm_glu(*args)
+    _check(lib().gemm_glu(*args, _stream(stream)))
+
+
+def gemm_glu_i8(a, w_gate, w_up, a_scale, gate_scale, up_scale, h, m, n, k, act="silu", h_dtype=None,
+                workspace=None, stream=None, validate_only=False):
+    """gemm_glu from 8-bit integers and their scales (see include/bsg.h)."""
+    dt = dtype_code(h_dtype if h_dtype is not None else h)
+    _need(a, "a", m * k, torch.int8)
+    _need(w_gate, "w_gate", n * k, torch.int8)
+    _need(w_up, "w_up", n * k, torch.int8)
+    _need(a_scale, "a_scale", 4 * m, torch.float32)
+    _need(gate_scale, "gate_scale", 4 * n, torch.float32)
+    _need(up_scale, "up_scale", 4 * n, torch.float32)
+    _need(h, "h", _out_bytes(dt, m * n), dt)
+    args = [_ptr(a), _ptr(w_gate), _ptr(w_up), _ptr(a_scale), _ptr(gate_scale), _ptr(up_scale), _ptr(h),
+            *_ws(workspace, "gemm_glu_i8", m, n, k), m, n, k, dt, _act(act)]
+    if validate_only:
+        return lib().bsg_validate_gemm_glu_i8(*args)
+    _check(lib().gemm_glu_i8(*args, _stream(stream)))
+
+
+def gemm_glu_bwd(dh, x, w_gate, w_up, g, u, dx, dw_gate, dw_up, m, n, k, act="silu", dtype=None,
+                 workspace=None, stream=None, validate_only=False):
+    """Gradients of gemm_glu from dh and the saved g and u (see include/bsg.h).
+    dx, or dw_gate and dw_up together, may be None."""
+    dt = dtype_code(dtype if dtype is not None else dh)
+    mn, mk, nk = _out_bytes(dt, m * n), _out_bytes(dt, m * k), _out_bytes(dt, n * k)
+    for t, name, b in ((dh, "dh", mn), (x, "x", mk), (w_gate, "w_gate", nk), (w_up, "w_up", nk), (g, "g", mn),
+                       (u, "u", mn), (dx, "dx", mk), (dw_gate, "dw_gate", nk), (dw_up, "dw_up", nk)):
+        _need(t, name, b, dt)
+    args = [_ptr(dh), _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(g), _ptr(u), _ptr(dx), _ptr(dw_gate), _ptr(dw_up),
+            *_ws(workspace, "gemm_glu_bwd", m, n, k), m, n, k, dt, _act(act)]
+    if validate_only:
+        return lib().bsg_validate_gemm_glu_bwd(*args)
+    _check(lib().gemm_glu_bwd(*args, _stream(stream)))

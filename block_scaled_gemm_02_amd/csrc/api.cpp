@@ -12,6 +12,7 @@
 #include <utility>
 
 #include "../../include/bsg.h"
+#include "ffn/ffn.hpp"
 #include "launch.hpp"
 
 namespace {
@@ -578,6 +579,214 @@ int gemm_proj_rope_mxfp8(const void *x, const void *w, const uint8_t *x_scale, c
                            in_dtype == BSG_E4M3 ? 1 : 0};
     return launch_status(bsg::launch_proj_rope(args, static_cast<hipStream_t>(stream)),
                          "gemm_proj_rope_mxfp8");
+}
+
+// ---------------------------------------------------------------------------
+// Feed-forward operators
+// ---------------------------------------------------------------------------
+// int32 sums of products of int8 are exact up to this K: 2^14 k < 2^31
+static constexpr int64_t kMaxI8K = 131056;
+
+static int check_ffn_sizes(int64_t m, int64_t n, int64_t k)
+{
+    if (m < 0 || n < 0 || k < 0) return fail(BSG_ERR_SHAPE, "negative size");
+    if (m > (1ll << 22) || n > (1ll << 20) || k > (1ll << 20))
+        return fail(BSG_ERR_UNSUPPORTED, "M=%lld, N=%lld, K=%lld: past 2^22 tokens or 2^20 channels", (long long)m,
+                    (long long)n, (long long)k);
+    return BSG_OK;
+}
+
+// output tiles of an (r, c) product: the grid's limit
+static int check_ffn_tiles(int64_t r, int64_t c)
+{
+    const int64_t tiles = ((r + 63) / 64) * ((c + 63) / 64);
+    if (tiles >= (1ll << 23)) return fail(BSG_ERR_UNSUPPORTED, "%lld output tiles exceed the launch limit", (long long)tiles);
+    return BSG_OK;
+}
+
+static int check_act(int act)
+{
+    if (act < BSG_ACT_SILU || act > BSG_ACT_RELU) return fail(BSG_ERR_SHAPE, "act %d is not a bsg_act", act);
+    return BSG_OK;
+}
+
+static int check_workspace(const void *ws, int64_t have, int op, int64_t m, int64_t n, int64_t k)
+{
+    const int64_t need = bsg_workspace_bytes(op, m, n, k);
+    if (need == 0) return BSG_OK;
+    if (!ws) return fail(BSG_ERR_NULLPTR, "a workspace of %lld bytes is required", (long long)need);
+    if (!aligned16(ws)) return fail(BSG_ERR_ALIGN, "workspace must be 16-byte aligned");
+    if (have < need)
+        return fail(BSG_ERR_SHAPE, "workspace holds %lld bytes; these sizes need %lld", (long long)have, (long long)need);
+    return BSG_OK;
+}
+
+static bool is_16bit(int dt) { return dt == BSG_F16 || dt == BSG_BF16; }
+static bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+int64_t bsg_workspace_bytes(int op, int64_t m, int64_t n, int64_t k)
+{
+    if (m < 0 || n < 0 || k < 0) return -1;
+    switch (op) {
+    case BSG_OP_GEMM_I8: return bsg::ffn::workspace_gemm_i8(m, n, k);
+    case BSG_OP_GEMM_GLU: return bsg::ffn::workspace_gemm_glu(m, n, k, false);
+    case BSG_OP_GEMM_GLU_I8: return bsg::ffn::workspace_gemm_glu(m, n, k, true);
+    case BSG_OP_GEMM_GLU_BWD: return bsg::ffn::workspace_gemm_glu_bwd(m, n, k);
+    default: return -1;
+    }
+}
+
+int bsg_validate_quant_i8(const void *x, int8_t *q, float *scale, int64_t m, int64_t k, int x_dtype)
+{
+    if (int r = check_ffn_sizes(m, 0, k)) return r;
+    if (!is_float_out(x_dtype)) return fail(BSG_ERR_DTYPE, "x_dtype %d is not fp32, fp16 or bf16", x_dtype);
+    if (k % 16) return fail(BSG_ERR_ALIGN, "K=%lld must be a multiple of 16", (long long)k);
+    if (m == 0) return BSG_OK;
+    if (!scale || (k && (!x || !q))) return fail(BSG_ERR_NULLPTR, "x, q and scale are required");
+    if (!aligned16(x) || !aligned16(q)) return fail(BSG_ERR_ALIGN, "x and q must be 16-byte aligned");
+    if (!aligned4(scale)) return fail(BSG_ERR_ALIGN, "scale must be 4-byte aligned");
+    return BSG_OK;
+}
+
+int quant_i8(const void *x, int8_t *q, float *scale, int64_t m, int64_t k, int x_dtype, void *stream)
+{
+    int st = bsg_validate_quant_i8(x, q, scale, m, k, x_dtype);
+    if (st) return st;
+    if ((st = check_device())) return st;
+    const bsg::ffn::QuantArgs args{x, q, scale, m, k, x_dtype};
+    return launch_status(bsg::ffn::launch_quant_i8(args, static_cast<hipStream_t>(stream)), "quant_i8");
+}
+
+int bsg_validate_gemm_i8(const int8_t *a, const int8_t *b, const float *a_scale, const float *b_scale,
+                         const void *bias, void *c, void *workspace, int64_t workspace_bytes, int64_t m,
+                         int64_t n, int64_t k, int bias_dtype, int c_dtype)
+{
+    if (int r = check_ffn_sizes(m, n, k)) return r;
+    if (!is_float_out(c_dtype)) return fail(BSG_ERR_DTYPE, "c_dtype %d is not fp32, fp16 or bf16", c_dtype);
+    if (bias && !is_float_out(bias_dtype)) return fail(BSG_ERR_DTYPE, "bias_dtype %d is not fp32, fp16 or bf16", bias_dtype);
+    if (k % 16 || (n * elem_bytes(c_dtype)) % 16)
+        return fail(BSG_ERR_ALIGN, "K=%lld and C rows of N=%lld must be multiples of 16 bytes", (long long)k, (long long)n);
+    if (k > kMaxI8K) return fail(BSG_ERR_UNSUPPORTED, "K=%lld: int32 sums are exact up to K=%lld", (long long)k, (long long)kMaxI8K);
+    if (int r = check_ffn_tiles(m, n)) return r;
+    if (m == 0 || n == 0) return BSG_OK;
+    if (!a_scale || !b_scale || !c || (k && (!a || !b)))
+        return fail(BSG_ERR_NULLPTR, "a, b, a_scale, b_scale and c are required");
+    if (!aligned16(a) || !aligned16(b) || !aligned16(c)) return fail(BSG_ERR_ALIGN, "a, b and c must be 16-byte aligned");
+    if (!aligned4(a_scale) || !aligned4(b_scale) ||
+        (bias && (reinterpret_cast<uintptr_t>(bias) & (uintptr_t)(elem_bytes(bias_dtype) - 1))))
+        return fail(BSG_ERR_ALIGN, "scales and bias must be aligned to their elements");
+    return check_workspace(workspace, workspace_bytes, BSG_OP_GEMM_I8, m, n, k);
+}
+
+int gemm_i8(const int8_t *a, const int8_t *b, const float *a_scale, const float *b_scale, const void *bias,
+            void *c, void *workspace, int64_t workspace_bytes, int64_t m, int64_t n, int64_t k,
+            int bias_dtype, int c_dtype, void *stream)
+{
+    int st = bsg_validate_gemm_i8(a, b, a_scale, b_scale, bias, c, workspace, workspace_bytes, m, n, k,
+                                  bias_dtype, c_dtype);
+    if (st) return st;
+    if ((st = check_device())) return st;
+    const bsg::ffn::I8Args args{a, b, a_scale, b_scale, bias, c, workspace, m, n, k, bias_dtype, c_dtype};
+    return launch_status(bsg::ffn::launch_gemm_i8(args, static_cast<hipStream_t>(stream)), "gemm_i8");
+}
+
+// Checks that both gated products share (scales aside)
+static int check_glu(const void *x, const void *wg, const void *wu, const void *h, int64_t m, int64_t n,
+                     int64_t k, bool in_i8, int dtype, int act)
+{
+    if (int r = check_ffn_sizes(m, n, k)) return r;
+    if (int r = check_act(act)) return r;
+    if (!is_16bit(dtype)) return fail(BSG_ERR_DTYPE, "dtype %d is not fp16 or bf16", dtype);
+    if (n % 8 || k % (in_i8 ? 16 : 8))
+        return fail(BSG_ERR_ALIGN, "N=%lld and K=%lld must make rows of a multiple of 16 bytes", (long long)n, (long long)k);
+    if (in_i8 && k > kMaxI8K)
+        return fail(BSG_ERR_UNSUPPORTED, "K=%lld: int32 sums are exact up to K=%lld", (long long)k, (long long)kMaxI8K);
+    if (int r = check_ffn_tiles(m, 2 * n)) return r;
+    if (m == 0 || n == 0) return BSG_OK;
+    if (!h || (k && (!x || !wg || !wu))) return fail(BSG_ERR_NULLPTR, "x, w_gate, w_up and h are required");
+    if (!aligned16(x) || !aligned16(wg) || !aligned16(wu) || !aligned16(h))
+        return fail(BSG_ERR_ALIGN, "x, w_gate, w_up and h must be 16-byte aligned");
+    return BSG_OK;
+}
+
+int bsg_validate_gemm_glu(const void *x, const void *w_gate, const void *w_up, void *h, void *g, void *u,
+                          void *workspace, int64_t workspace_bytes, int64_t m, int64_t n, int64_t k,
+                          int dtype, int act)
+{
+    if (int r = check_glu(x, w_gate, w_up, h, m, n, k, false, dtype, act)) return r;
+    if (m == 0 || n == 0) return BSG_OK;
+    if (!g != !u) return fail(BSG_ERR_NULLPTR, "g and u are given together or not at all");
+    if (!aligned16(g) || !aligned16(u)) return fail(BSG_ERR_ALIGN, "g and u must be 16-byte aligned");
+    return check_workspace(workspace, workspace_bytes, BSG_OP_GEMM_GLU, m, n, k);
+}
+
+int gemm_glu(const void *x, const void *w_gate, const void *w_up, void *h, void *g, void *u, void *workspace,
+             int64_t workspace_bytes, int64_t m, int64_t n, int64_t k, int dtype, int act, void *stream)
+{
+    int st = bsg_validate_gemm_glu(x, w_gate, w_up, h, g, u, workspace, workspace_bytes, m, n, k, dtype, act);
+    if (st) return st;
+    if ((st = check_device())) return st;
+    const bsg::ffn::GluArgs args{x, w_gate, w_up, nullptr, nullptr, nullptr, h, g, u, workspace, m, n, k, 0, dtype, act};
+    return launch_status(bsg::ffn::launch_gemm_glu(args, static_cast<hipStream_t>(stream)), "gemm_glu");
+}
+
+int bsg_validate_gemm_glu_i8(const int8_t *a, const int8_t *w_gate, const int8_t *w_up, const float *a_scale,
+                             const float *gate_scale, const float *up_scale, void *h, void *workspace,
+                             int64_t workspace_bytes, int64_t m, int64_t n, int64_t k, int h_dtype, int act)
+{
+    if (int r = check_glu(a, w_gate, w_up, h, m, n, k, true, h_dtype, act)) return r;
+    if (m == 0 || n == 0) return BSG_OK;
+    if (!a_scale || !gate_scale || !up_scale)
+        return fail(BSG_ERR_NULLPTR, "a_scale, gate_scale and up_scale are required");
+    if (!aligned4(a_scale) || !aligned4(gate_scale) || !aligned4(up_scale))
+        return fail(BSG_ERR_ALIGN, "scales must be 4-byte aligned");
+    return check_workspace(workspace, workspace_bytes, BSG_OP_GEMM_GLU_I8, m, n, k);
+}
+
+int gemm_glu_i8(const int8_t *a, const int8_t *w_gate, const int8_t *w_up, const float *a_scale,
+                const float *gate_scale, const float *up_scale, void *h, void *workspace,
+                int64_t workspace_bytes, int64_t m, int64_t n, int64_t k, int h_dtype, int act, void *stream)
+{
+    int st = bsg_validate_gemm_glu_i8(a, w_gate, w_up, a_scale, gate_scale, up_scale, h, workspace,
+                                      workspace_bytes, m, n, k, h_dtype, act);
+    if (st) return st;
+    if ((st = check_device())) return st;
+    const bsg::ffn::GluArgs args{a, w_gate, w_up, a_scale, gate_scale, up_scale, h, nullptr, nullptr, workspace,
+                                 m, n, k, 1, h_dtype, act};
+    return launch_status(bsg::ffn::launch_gemm_glu(args, static_cast<hipStream_t>(stream)), "gemm_glu_i8");
+}
+
+int bsg_validate_gemm_glu_bwd(const void *dh, const void *x, const void *w_gate, const void *w_up,
+                              const void *g, const void *u, void *dx, void *dw_gate, void *dw_up,
+                              void *workspace, int64_t workspace_bytes, int64_t m, int64_t n, int64_t k,
+                              int dtype, int act)
+{
+    if (int r = check_ffn_sizes(m, n, k)) return r;
+    if (int r = check_act(act)) return r;
+    if (!is_16bit(dtype)) return fail(BSG_ERR_DTYPE, "dtype %d is not fp16 or bf16", dtype);
+    if (n % 8 || k % 8)
+        return fail(BSG_ERR_ALIGN, "N=%lld and K=%lld must be multiples of 8", (long long)n, (long long)k);
+    if (int r = check_ffn_tiles(m, k)) return r;
+    if (int r = check_ffn_tiles(2 * n, k)) return r;
+    if (!dw_gate != !dw_up) return fail(BSG_ERR_NULLPTR, "dw_gate and dw_up are given together or not at all");
+    const bool some = m && n;      // anything to read
+    if (some && ((!dh || !g || !u) || (dx && k && (!w_gate || !w_up)) || (dw_gate && k && !x)))
+        return fail(BSG_ERR_NULLPTR, "dh, g and u are required, the weights for dx, and x for dw_gate and dw_up");
+    for (const void *p : {dh, x, w_gate, w_up, g, u, (const void *)dx, (const void *)dw_gate, (const void *)dw_up})
+        if (!aligned16(p)) return fail(BSG_ERR_ALIGN, "every tensor must be 16-byte aligned");
+    return check_workspace(workspace, workspace_bytes, BSG_OP_GEMM_GLU_BWD, m, n, k);
+}
+
+int gemm_glu_bwd(const void *dh, const void *x, const void *w_gate, const void *w_up, const void *g,
+                 const void *u, void *dx, void *dw_gate, void *dw_up, void *workspace,
+                 int64_t workspace_bytes, int64_t m, int64_t n, int64_t k, int dtype, int act, void *stream)
+{
+    int st = bsg_validate_gemm_glu_bwd(dh, x, w_gate, w_up, g, u, dx, dw_gate, dw_up, workspace,
+                                       workspace_bytes, m, n, k, dtype, act);
+    if (st) return st;
+    if ((st = check_device())) return st;
+    const bsg::ffn::GluBwdArgs args{dh, x, w_gate, w_up, g, u, dx, dw_gate, dw_up, workspace, m, n, k, dtype, act};
+    return launch_status(bsg::ffn::launch_gemm_glu_bwd(args, static_cast<hipStream_t>(stream)), "gemm_glu_bwd");
 }
 
 }  // extern "C"

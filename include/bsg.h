@@ -1,7 +1,7 @@
 /*
  * bsg.h -- block-scaled GEMM family for AMD Instinct MI355X (gfx950).
  *
- * A C ABI over hand-written HIP kernels.  Four operations, each the
+ * A C ABI over hand-written HIP kernels.  Five operations, each the
  * problem statement of one cuDNN frontend "GEMM fusions" documentation page:
  *
  *   gemm_amax             "GEMM + Amax (SM100)"
@@ -9,6 +9,11 @@
  *   grouped_gemm_srelu    "Grouped GEMM + sReLU (SM100)"
  *   grouped_gemm_dswiglu  "Grouped GEMM + dSwiGLU (SM100)"
  *   gemm_proj_rope_mxfp8  "GEMM + RoPE + MXFP8 Projection (SM100)"
+ *
+ * and the operators of a gated feed-forward block (their own section below):
+ *
+ *   quant_i8, gemm_i8, gemm_glu_i8    8-bit integers with scales
+ *   gemm_glu, gemm_glu_bwd            16-bit, forward and backward
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -370,6 +375,116 @@ int bsg_validate_gemm_proj_rope_mxfp8(const void *x, const void *w, const uint8_
  * for the hot path. */
 int bsg_check_padded_offsets(const int32_t *padded_offsets, int64_t num_experts, int64_t m,
                              void *stream);
+
+/* -------------------------------------------------------------------------
+ * Feed-forward operators: what a gated feed-forward block runs in training
+ * (16-bit operands) and in serving (8-bit integers with scales).  All tensors
+ * are dense and row-major; weights are (out, in), as for the other entry
+ * points.  M counts tokens and takes any value >= 0; rows are whole 16-byte
+ * pieces (ALIGN otherwise), so N and K are multiples of 8 (16-bit), K of 16
+ * (integers), N of 4 (fp32 C).  K = 0 is an empty sum.  Sums are held in fp32
+ * (16-bit operands) or int32 (integers, exact).  Sizes past 2^22 tokens, 2^20
+ * channels or 2^23 64x64 output tiles return UNSUPPORTED.
+ *
+ * `workspace` is scratch of at least bsg_workspace_bytes(op, m, n, k) bytes,
+ * 16-byte aligned, whose contents do not matter before or after a call; calls
+ * that may run at the same time need one each.  NULL where that is 0 bytes.
+ * ------------------------------------------------------------------------- */
+typedef enum bsg_act {
+    BSG_ACT_SILU = 0,       /* x / (1 + exp(-x)) */
+    BSG_ACT_GELU_TANH = 1,  /* x/2 (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) */
+    BSG_ACT_RELU = 2        /* max(x, 0) */
+} bsg_act;
+
+typedef enum bsg_op {
+    BSG_OP_GEMM_I8 = 0,
+    BSG_OP_GEMM_GLU = 1,
+    BSG_OP_GEMM_GLU_I8 = 2,
+    BSG_OP_GEMM_GLU_BWD = 3
+} bsg_op;
+
+/* Scratch bytes that the operator takes at these sizes (enough for every
+ * type and option); -1 for an unknown op or a negative size. */
+int64_t bsg_workspace_bytes(int op, int64_t m, int64_t n, int64_t k);
+
+/*
+ * quant_i8 -- rows to symmetric 8-bit integers, one scale a row:
+ *     t = max(max_k |x[m,k]|, 2^-100)
+ *     scale[m] = t / 127          q[m,k] = rint(x[m,k] * (127 / t))
+ *   each step one fp32 operation, rint to nearest even, so |q| <= 127.
+ *   A row that holds NaN (infinity) gets the scale NaN (infinity), and the
+ *   codes of such a row are 0: its dequantised values are NaN.
+ *   x (m, k) fp32 / fp16 / bf16;  q (m, k) int8;  scale (m,) fp32.
+ *   K is a multiple of 16.  Quantises weights too (a row is a channel).
+ */
+int quant_i8(const void *x, int8_t *q, float *scale, int64_t m, int64_t k, int x_dtype,
+             void *stream);
+
+/*
+ * gemm_i8 -- product of 8-bit integers with a scale for each token and channel:
+ *     c[m,n] = (sum_k a[m,k] b[n,k]) * a_scale[m] * b_scale[n] + bias[n]
+ *   a (m, k), b (n, k) int8;  a_scale (m,), b_scale (n,) fp32;  bias (n,)
+ *   fp32 / fp16 / bf16 or NULL;  c (m, n) fp32 / fp16 / bf16.
+ *   The sum is exact in int32, so k <= 131056 (UNSUPPORTED past it).
+ */
+int gemm_i8(const int8_t *a, const int8_t *b, const float *a_scale, const float *b_scale,
+            const void *bias, void *c, void *workspace, int64_t workspace_bytes, int64_t m,
+            int64_t n, int64_t k, int bias_dtype, int c_dtype, void *stream);
+
+/*
+ * gemm_glu -- both projections of a gated block, the activation and the
+ * product in one pass:
+ *     G = X Wg^T,   U = X Wu^T,   H = act(G) * U
+ *   x (m, k), w_gate and w_up (n, k), h (m, n): all fp16 or all bf16.
+ *   g, u (m, n): the same type, both or neither (NULL); what the backward
+ *   pass reads.  H is formed from the unrounded G and U.
+ */
+int gemm_glu(const void *x, const void *w_gate, const void *w_up, void *h, void *g, void *u,
+             void *workspace, int64_t workspace_bytes, int64_t m, int64_t n, int64_t k,
+             int dtype, int act, void *stream);
+
+/*
+ * gemm_glu_i8 -- gemm_glu from 8-bit integers:
+ *     G[m,n] = (sum_k a[m,k] w_gate[n,k]) * a_scale[m] * gate_scale[n],  U alike.
+ *   a, w_gate, w_up int8; the scales fp32; h (m, n) fp16 or bf16; k as gemm_i8.
+ */
+int gemm_glu_i8(const int8_t *a, const int8_t *w_gate, const int8_t *w_up, const float *a_scale,
+                const float *gate_scale, const float *up_scale, void *h, void *workspace,
+                int64_t workspace_bytes, int64_t m, int64_t n, int64_t k, int h_dtype, int act,
+                void *stream);
+
+/*
+ * gemm_glu_bwd -- the gradients of gemm_glu from dH and the saved G and U:
+ *     dG = dH * U * act'(G)         dU = dH * act(G)
+ *     dX = dG Wg + dU Wu            dWg = dG^T X       dWu = dU^T X
+ *   All tensors fp16 or all bf16.  dG and dU are formed in fp32 and rounded
+ *   once to that type, which the matrix cores read.  act'(0) of ReLU is 0.
+ *   dx may be NULL (no input gradient), and so may dw_gate and dw_up together
+ *   (frozen weights; x may then be NULL too).  Outputs are overwritten, and
+ *   are the same from call to call: no sum depends on the order of arrival.
+ */
+int gemm_glu_bwd(const void *dh, const void *x, const void *w_gate, const void *w_up,
+                 const void *g, const void *u, void *dx, void *dw_gate, void *dw_up,
+                 void *workspace, int64_t workspace_bytes, int64_t m, int64_t n, int64_t k,
+                 int dtype, int act, void *stream);
+
+/* Host-only checks of the same arguments minus the stream. */
+int bsg_validate_quant_i8(const void *x, int8_t *q, float *scale, int64_t m, int64_t k, int x_dtype);
+int bsg_validate_gemm_i8(const int8_t *a, const int8_t *b, const float *a_scale,
+                         const float *b_scale, const void *bias, void *c, void *workspace,
+                         int64_t workspace_bytes, int64_t m, int64_t n, int64_t k, int bias_dtype,
+                         int c_dtype);
+int bsg_validate_gemm_glu(const void *x, const void *w_gate, const void *w_up, void *h, void *g,
+                          void *u, void *workspace, int64_t workspace_bytes, int64_t m, int64_t n,
+                          int64_t k, int dtype, int act);
+int bsg_validate_gemm_glu_i8(const int8_t *a, const int8_t *w_gate, const int8_t *w_up,
+                             const float *a_scale, const float *gate_scale, const float *up_scale,
+                             void *h, void *workspace, int64_t workspace_bytes, int64_t m,
+                             int64_t n, int64_t k, int h_dtype, int act);
+int bsg_validate_gemm_glu_bwd(const void *dh, const void *x, const void *w_gate, const void *w_up,
+                              const void *g, const void *u, void *dx, void *dw_gate, void *dw_up,
+                              void *workspace, int64_t workspace_bytes, int64_t m, int64_t n,
+                              int64_t k, int dtype, int act);
 
 /* Static text for a status code. */
 const char *bsg_status_string(int status);
