@@ -1,0 +1,343 @@
+// The matrix-product tile of the feed-forward operators: a workgroup of four
+// wave64s computes a (64 MI) x (64 NB) tile, each wave a (32 MI) x (32 NB)
+// quadrant in 32x32 MFMA blocks whose accumulators stay in registers.
+//
+// Operands are bf16, fp16 or int8, and any of them is read in 16-byte chunks:
+// one MFMA of 32x32x16 (16 bits) or 32x32x32 (8 bits) takes one chunk a lane
+// and operand, lane (r = l%32, g = l/32) holding K bytes [16g, 16g + 16) of
+// row r.  K advances in pairs of 128 bytes a row (one whole line), in two
+// steps of 64 bytes (two MFMAs a block).
+//
+// The LDS holds a ring of NS pair slots, filled by direct-to-LDS loads
+// (buffer_load_dwordx4 ... lds) that no register passes through; reads past a
+// row, a tensor or the K range return zeros (buffer range check), which is
+// all that ragged sizes need.  Within a pair's second step the slot of the
+// pair is free (its last fragments are in registers, and a barrier says so
+// for all waves), and the loads of the pair NS further on go out between the
+// MFMAs.  The fragments of the next step are read between the MFMAs too.
+//
+// k-major panel (rows of K): row r at 128 r, its 16-byte chunk c at position
+// c ^ s(r), s(r) = (r%8) ^ ((r/8)%2), so that the 16 lanes that a 128-bit
+// read serves at once cover all 64 banks.
+// mn-major panel (16-bit; rows of M or N at each K): K row kk at (2 T) kk, its
+// 64-byte block b at b ^ (kk%4); the transposing read (ds_read_b64_tr_b16)
+// of a half wave takes 64 bytes from each of 4 consecutive K rows, which the
+// exchange puts on different banks.
+#pragma once
+#include "act.hpp"
+
+namespace bsg {
+namespace ffn {
+
+enum In : int { IN_BF16 = 0, IN_F16 = 1, IN_I8 = 2 };
+constexpr int in_bytes(int in) { return in == IN_I8 ? 1 : 2; }
+constexpr int dt_of(int in) { return in == IN_F16 ? DT_F16 : DT_BF16; }
+
+template <int IN>
+__device__ __forceinline__ f32x16 mfma32(const i32x4 &b, const i32x4 &a, const f32x16 &acc)
+{
+    if constexpr (IN == IN_BF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a), acc, 0, 0, 0);
+    else if constexpr (IN == IN_F16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, b), __builtin_bit_cast(f16x8, a), acc, 0, 0, 0);
+    else
+        return __builtin_bit_cast(f32x16, __builtin_amdgcn_mfma_i32_32x32x32_i8(b, a, __builtin_bit_cast(i32x16, acc), 0, 0, 0));
+}
+
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)); }
+
+// Pairs of a K extent in bytes; an empty sum runs one, of zeros.
+__device__ __forceinline__ int pairs_of(int64_t kbytes) { return kbytes > 128 ? (int)((kbytes + 127) / 128) : 1; }
+
+// Readable bytes as a buffer resource takes them.
+__device__ __forceinline__ uint32_t clamp_bytes(int64_t b) { return b <= 0 ? 0u : (b < 0x7FFFFFFF ? (uint32_t)b : 0x7FFFFFFFu); }
+
+// One wave's share of the loads of a T-row panel: T/32 loads of 1 KB a pair.
+// k-major: rows T/4 w ...  of the panel, base at the first of them, `bytes`
+// readable from there, K bytes [0, klimit) of each row.  mn-major: base at
+// the tile's first column in K row 0, `cols` of its columns exist.
+template <bool KM, int T>
+struct Loader {
+    static constexpr int L = T / 32;
+    const uint8_t *base;
+    int64_t bytes, step;
+    i32x4 r;
+    uint32_t v[L], pv, klimit, chunk[2], add[2], padd;
+
+    __device__ __forceinline__ void init_k(const uint8_t *b, int64_t n, int64_t ld, int64_t kbytes, int w, int lane)
+    {
+        base = b;
+        bytes = n;
+        klimit = (uint32_t)kbytes;
+        r = make_rsrc_words(base, clamp_bytes(bytes));
+        const uint32_t row = (uint32_t)lane >> 3, c = ((uint32_t)lane & 7) ^ row ^ ((uint32_t)(L * w) & 1);
+        chunk[0] = 16 * c;
+        chunk[1] = chunk[0] ^ 16;
+#pragma unroll
+        for (int q = 0; q < L; ++q) v[q] = (8 * q + row) * (uint32_t)ld + chunk[q & 1];
+        pv = lane < T / 4 ? (uint32_t)lane * (uint32_t)ld : kOOB;
+    }
+    __device__ __forceinline__ void init_mn(const uint8_t *b, int64_t n, int64_t ld, int64_t cols, int w, int lane)
+    {
+        base = b;
+        bytes = n;
+        step = 64 * ld;
+        const uint32_t valid = cols < T ? (uint32_t)(2 * cols) : 2u * T;
+#pragma unroll
+        for (int q = 0; q < L; ++q) {
+            const uint32_t p = 1024u * (L * w + q) + 16u * (uint32_t)lane, kk = p / (2 * T), o = p % (2 * T);
+            const uint32_t col = o ^ (64u * (kk & 3));
+            v[q] = col < valid ? kk * (uint32_t)ld + col : kOOB;
+        }
+        constexpr uint32_t LPR = T / 64;       // lines of a K row
+        const uint32_t line = 128u * ((uint32_t)lane % LPR);
+        pv = (uint32_t)lane < 16 * LPR && line < valid ? (16u * w + (uint32_t)lane / LPR) * (uint32_t)ld + line : kOOB;
+    }
+    // Aims the loads at a pair.
+    __device__ __forceinline__ void seek(int pair)
+    {
+        if constexpr (KM) {
+            const uint32_t kb = (uint32_t)pair * 128u;
+            add[0] = kb + chunk[0] < klimit ? kb : kOOB;
+            add[1] = kb + chunk[1] < klimit ? kb : kOOB;
+            padd = kb < klimit ? kb : kOOB;
+        } else {
+            const int64_t off = (int64_t)pair * step;
+            r = make_rsrc_words(base + off, clamp_bytes(bytes - off));
+            padd = 0;
+        }
+    }
+    template <int Q>
+    __device__ __forceinline__ void load(uint8_t *panel, int w) const
+    {
+        lds_load16(r, panel + 1024 * (L * w + Q), v[Q] + (KM ? add[Q & 1] : 0u));
+    }
+    // Touches the lines of the pair, so that its loads find them in the L2.
+    __device__ __forceinline__ void prefetch(uint8_t *sink, int w) const { lds_load4(r, sink + 256 * w, pv + padd); }
+};
+
+// Fragment reads of one wave from a panel: C chunks of 32 rows each.
+template <bool KM, int T, int C>
+struct Reader {
+    static constexpr int kReads = KM ? 2 * C : 4 * C;      // of a step
+    uint32_t off[KM ? 4 : C];
+    // row0: the wave's first row (column) in the panel
+    __device__ __forceinline__ void init(int row0, int lane)
+    {
+        if constexpr (KM) {
+            const uint32_t r = (uint32_t)lane & 31, g = (uint32_t)lane >> 5, s = (r & 7) ^ ((r >> 3) & 1);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) off[c] = ((uint32_t)row0 + r) * 128u + 16u * ((2u * c + g) ^ s);
+        } else {
+            const uint32_t G = (uint32_t)lane >> 4, s = (uint32_t)lane & 15, kk = 8u * (G >> 1) + (s >> 2);
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                off[c] = kk * (2u * T) + 64u * (((uint32_t)row0 / 32u + c) ^ (kk & 3)) + 32u * (G & 1) + 8u * (s & 3);
+        }
+    }
+    // Read Q of the step in half H of a pair.
+    template <int H, int Q>
+    __device__ __forceinline__ void read(i32x4 (&f)[C][2], const uint8_t *panel) const
+    {
+        if constexpr (KM) {
+            constexpr int c = Q / 2, h = Q % 2;
+            f[c][h] = *reinterpret_cast<const i32x4 *>(panel + off[2 * H + h] + 4096 * c);
+        } else {
+            constexpr int c = Q / 4, h = (Q / 2) % 2, e = Q % 2;
+            const uint8_t *p = panel + off[c] + (32 * H + 16 * h + 4 * e) * 2 * T;
+            const auto x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(lds_void *)p);
+            const i32x2_t u = __builtin_bit_cast(i32x2_t, x);
+            if constexpr (e == 0) {
+                f[c][h].x = u.x;
+                f[c][h].y = u.y;
+            } else {
+                f[c][h].z = u.x;
+                f[c][h].w = u.y;
+            }
+        }
+    }
+};
+
+template <int MI, int NB>
+struct Frag {
+    i32x4 a[MI][2], b[NB][2];
+};
+
+// The ring of a tile and the K loop over it.
+template <int IN, bool AK, bool BK, int MI, int NB, int NS, bool PF>
+struct Tile {
+    static constexpr int TM = 64 * MI, TN = 64 * NB;
+    static constexpr int kA = TM * 128, kSlot = kA + TN * 128, kRing = NS * kSlot, kLds = kRing + (PF ? 1024 : 0);
+    static constexpr int kStage = kRing / 4 & ~15;          // epilogue staging bytes of a wave
+    typedef Loader<AK, TM> LA;
+    typedef Loader<BK, TN> LB;
+    static constexpr int LP = LA::L + LB::L;                // loads of a pair and wave
+    static constexpr int kM = 2 * MI * NB;                  // MFMAs of a step
+    Reader<AK, TM, MI> ra;
+    Reader<BK, TN, NB> rb;
+    static constexpr int kR = Reader<AK, TM, MI>::kReads + Reader<BK, TN, NB>::kReads;
+    static constexpr int kRSpan = kM * 3 / 4 > 0 ? kM * 3 / 4 : 1;
+
+    template <int H, int Q>
+    __device__ __forceinline__ void read1(Frag<MI, NB> &f, const uint8_t *slot) const
+    {
+        constexpr int RA = Reader<AK, TM, MI>::kReads;
+        if constexpr (Q < RA) ra.template read<H, Q>(f.a, slot);
+        else rb.template read<H, Q - RA>(f.b, slot + kA);
+    }
+    template <int Q>
+    __device__ __forceinline__ void load1(const LA &la, const LB &lb, uint8_t *slot, int w) const
+    {
+        if constexpr (Q < LA::L) la.template load<Q>(slot, w);
+        else lb.template load<Q - LA::L>(slot + kA, w);
+    }
+
+    // One step: MFMAs on cur, fragments of the next step (half NH of rslot)
+    // into nxt, and, in a pair's second step, the loads of a later pair.
+    template <bool ODD, class Seek>
+    __device__ __forceinline__ void step(f32x16 (&acc)[MI][NB], Frag<MI, NB> &cur, Frag<MI, NB> &nxt, LA &la, LB &lb,
+                                         const uint8_t *rslot, uint8_t *lslot, uint8_t *sink, int w, Seek &&seek)
+    {
+        if constexpr (ODD) {
+            // the next pair has landed: what may be in flight is the pairs after it and one prefetch
+            s_wait_vm<(NS - 2) * LP + (PF ? 1 : 0)>();
+            s_wait_lgkm0();
+            __builtin_amdgcn_s_barrier();
+        } else {
+            s_wait_lgkm0();
+            seek();                  // aim at the pair that the next step loads
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        static_for<kM>([&](auto mm) {
+            constexpr int m = decltype(mm)::value, S = m / (MI * NB), i = (m % (MI * NB)) / NB, j = m % NB;
+            acc[i][j] = mfma32<IN>(cur.b[j][S], cur.a[i][S], acc[i][j]);
+            if constexpr (m < kRSpan) {
+                static_for<(kR * (m + 1)) / kRSpan - (kR * m) / kRSpan>([&](auto rr) {
+                    read1<ODD ? 0 : 1, (kR * m) / kRSpan + decltype(rr)::value>(nxt, rslot);
+                });
+            }
+            if constexpr (ODD) {
+                static_for<(LP * (m + 1)) / kM - (LP * m) / kM>([&](auto ll) {
+                    load1<(LP * m) / kM + decltype(ll)::value>(la, lb, lslot, w);
+                });
+            } else if constexpr (PF && m == 0) {
+                la.prefetch(sink, w);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    }
+
+    // acc = sum over np >= 1 pairs.  seek(p) aims la and lb at the p-th pair,
+    // which past the last one has to read nothing.  The loop body is one block
+    // without branches and runs at least once.
+    template <class Seek>
+    __device__ __forceinline__ void run(f32x16 (&acc)[MI][NB], uint8_t *ring, LA &la, LB &lb, int np, Seek &&seek)
+    {
+        const int lane = threadIdx.x & 63, w = wave_id();
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+        ra.init(32 * MI * (w >> 1), lane);
+        rb.init(32 * NB * (w & 1), lane);
+        uint8_t *const sink = ring + kRing;
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+            seek(s);
+            static_for<LP>([&](auto q) { load1<decltype(q)::value>(la, lb, ring + s * kSlot, w); });
+        }
+        s_wait_vm<(NS - 1) * LP>();
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        Frag<MI, NB> fx, fy;
+        static_for<kR>([&](auto q) { read1<0, decltype(q)::value>(fx, ring); });
+        uint8_t *slot = ring;
+        int pair = 0;
+        do {
+            uint8_t *const next = slot == ring + (NS - 1) * kSlot ? ring : slot + kSlot;
+            step<false>(acc, fx, fy, la, lb, slot, slot, sink, w, [&] { seek(pair + NS); });
+            step<true>(acc, fy, fx, la, lb, next, slot, sink, w, [] {});
+            slot = next;
+        } while (++pair < np);
+        s_wait_vm<0>();
+        s_wait_lgkm0();
+        __builtin_amdgcn_s_barrier();       // the ring is free: the epilogue stages in it
+        __builtin_amdgcn_sched_barrier(0);
+    }
+};
+
+// Order of tiles: workgroup b runs on XCD b % 8, 32 tiles of an XCD at a time
+// (one workgroup a CU).  XCDs take runs of 32 tiles in turn; tiles go in
+// squares of 16 x 16, a square in strips of 4 rows, so that an XCD's run is
+// 4 x 8 tiles, whose 12 panels its L2 streams once, and the 8 runs that are
+// at work together are a square, whose 32 panels come from HBM once.
+struct TileAt {
+    int m, n;
+};
+__device__ __forceinline__ TileAt tile_at(uint32_t b, uint32_t mt, uint32_t nt)
+{
+    constexpr uint32_t R = 256, Q = 16, G = 4;
+    const uint32_t tiles = mt * nt;
+    uint32_t s = b;
+    if (b < tiles - tiles % R) s = b / R * R + b % 8 * 32 + b % R / 8;
+    const uint32_t sq = s / (Q * nt), r = s % (Q * nt), rows = min(Q, mt - sq * Q);
+    const uint32_t c = r / (rows * Q), r2 = r % (rows * Q), cols = min(Q, nt - c * Q);
+    const uint32_t st = r2 / (G * cols), r3 = r2 % (G * cols), g = min(G, rows - st * G);
+    return {(int)(sq * Q + st * G + r3 % g), (int)(c * Q + r3 / g)};
+}
+
+// Holds a row of accumulator blocks in their AGPRs up to here: the compiler
+// otherwise reads all 256 at the end of the K loop and spills the fragments.
+template <int NB>
+__device__ __forceinline__ void pin(f32x16 (&acc)[NB])
+{
+#pragma unroll
+    for (int j = 0; j < NB; ++j) asm volatile("" : "+a"(acc[j]));
+}
+
+// Epilogue: a 32-row block of a wave's quadrant goes through LDS, so that
+// whole row segments are stored.  stage_block writes value(j, q), the four
+// columns 32j + 8q + 4g .. + 3 of this lane's row, W blocks of 32 columns;
+// flush_block stores the staged rows at dst (row r at dst + r row_bytes),
+// `rows` of which exist, `col_bytes` of each.
+template <int DT, int W, class F>
+__device__ __forceinline__ void stage_block(uint8_t *reg, int lane, F &&value)
+{
+    constexpr int ES = es_of<DT>();
+    uint8_t *row = reg + (lane & 31) * StageGeom<ES, W>::RBP + 4 * (lane >> 5) * ES;
+    static_for<W>([&](auto jj) {
+        constexpr int j = decltype(jj)::value;
+        static_for<4>([&](auto qq) {
+            constexpr int q = decltype(qq)::value;
+            const float4 x = value(jj, qq);
+            *reinterpret_cast<typename Quad<ES>::T *>(row + (32 * j + 8 * q) * ES) = pack_quad<DT>(x.x, x.y, x.z, x.w);
+        });
+    });
+}
+template <int ES, int W>
+__device__ __forceinline__ void flush_block(const uint8_t *reg, void *dst, uint32_t row_bytes, int rows, int col_bytes,
+                                            int lane)
+{
+    typedef StageGeom<ES, W> G;
+    static_assert(64 % G::LPR == 0 && 32 % G::RPI == 0, "whole rows a store");
+    const int lr = lane / G::LPR, cb = lane % G::LPR * 16;
+    const uint64_t base = (uint64_t)(uintptr_t)dst;
+    void *const udst = (void *)(uintptr_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(base >> 32)) << 32) |
+                                           (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)base));
+    const uint32_t n = (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)max(0, min(rows, 32)) * row_bytes));
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(udst, (short)0, (int)n, 0x00020000);
+    const uint32_t voff = cb < col_bytes ? (uint32_t)lr * row_bytes + (uint32_t)cb : kOOB;
+    // streamed past the L2 (nt) where a wave writes whole 128-byte lines: it
+    // is left to the operand panels
+    constexpr int kNT = G::RB % 128 == 0 ? 2 : 0;
+#pragma unroll
+    for (int k = 0; k < G::NK; ++k) {
+        const i32x4 v = *reinterpret_cast<const i32x4 *>(reg + (lr + k * G::RPI) * G::RBP + cb);
+        __builtin_amdgcn_raw_buffer_store_b128(v, rs, voff + (uint32_t)(k * G::RPI) * row_bytes, 0, kNT);
+    }
+}
+
+}  // namespace ffn
+}  // namespace bsg
