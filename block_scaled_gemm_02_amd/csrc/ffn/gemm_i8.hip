@@ -1,5 +1,5 @@
 // gemm_i8: C = (A B^T) * a_scale * b_scale + bias from 8-bit integers.
-#include "tile.hpp"
+#include "few.hpp"
 
 namespace bsg {
 namespace ffn {
@@ -73,6 +73,33 @@ __global__ __launch_bounds__(256, MI *NB == 16 ? 1 : 2) void k_i8(I8Args p, int 
     static_assert(kReg + 8 * 64 * CL <= T::kStage, "the staging fits the wave's part of the ring");
 }
 
+template <int CT, int RB, int MB, int U>
+__global__ __launch_bounds__(kFewThreads) void k_i8_few(I8Args p)
+{
+    __shared__ __attribute__((aligned(16))) float red[kFewWaves * 16 * MB * 16 * RB];
+    const int lane = threadIdx.x & 63;
+    const int64_t c0 = 16ll * RB * blockIdx.x;
+    const uint8_t *wrow[RB], *xrow[MB];
+#pragma unroll
+    for (int b = 0; b < RB; ++b) wrow[b] = (const uint8_t *)p.b + min(c0 + 16 * b + (lane & 15), p.n - 1) * p.k;
+#pragma unroll
+    for (int b = 0; b < MB; ++b) xrow[b] = (const uint8_t *)p.a + min((int64_t)16 * b + (lane & 15), p.m - 1) * p.k;
+    few_sums<IN_I8, RB, MB, U>(red, wrow, xrow, (int)p.k);
+    for (int i = threadIdx.x; i < 16 * RB * (int)p.m; i += kFewThreads) {
+        const int ch = i % (16 * RB), tk = i / (16 * RB);
+        const int64_t c = c0 + ch;
+        if (c >= p.n) continue;
+        const float bias = p.bias ? load_float(p.bias, c, p.bias_dtype) : 0.0f;
+        store_one<CT>(p.c, tk * p.n + c, few_join<IN_I8, RB, MB>(red, tk, ch) * p.a_scale[tk] * p.b_scale[c] + bias);
+    }
+}
+
+template <int CT, int RB, int MB, int U>
+void go_few(const I8Args &a, hipStream_t s)
+{
+    k_i8_few<CT, RB, MB, U><<<(unsigned)((a.n + 16 * RB - 1) / (16 * RB)), kFewThreads, 0, s>>>(a);
+}
+
 template <int CT, int MI, int NB, int NS, bool PF>
 void go(const I8Args &a, hipStream_t s)
 {
@@ -90,7 +117,10 @@ hipError_t launch_gemm_i8(const I8Args &a, hipStream_t s)
     const bool big = (a.m + 255) / 256 * ((a.n + 255) / 256) >= 128;
     auto by_tile = [&](auto ct) {
         constexpr int C = decltype(ct)::value;
-        if (big) go<C, 4, 4, 2, true>(a, s);
+        if (a.m <= 16) go_few<C, 1, 1, 4>(a, s);
+        else if (a.m <= 32) go_few<C, 1, 2, 2>(a, s);
+        else if (a.m <= 64) go_few<C, 2, 4, 2>(a, s);
+        else if (big) go<C, 4, 4, 2, true>(a, s);
         else go<C, 2, 2, 4, false>(a, s);
     };
     if (a.c_dtype == DT_F32) by_tile(std::integral_constant<int, DT_F32>{});

@@ -1,5 +1,5 @@
 // gemm_glu, gemm_glu_i8: H = act(X Wg^T) * (X Wu^T).
-#include "tile.hpp"
+#include "few.hpp"
 
 namespace bsg {
 namespace ffn {
@@ -91,6 +91,47 @@ __global__ __launch_bounds__(256, MI *NB == 16 ? 1 : 2) void k_glu(GluArgs p, in
     static_assert(3 * kReg + 512 <= T::kStage, "the staging fits the wave's part of the ring");
 }
 
+// A few tokens: of a workgroup's 16 RB weight rows the first half are gate
+// rows and the second the up rows of the same channels.
+template <int IN, int DT, int ACT, bool SAVE, int RB, int MB, int U>
+__global__ __launch_bounds__(kFewThreads) void k_glu_few(GluArgs p)
+{
+    __shared__ __attribute__((aligned(16))) float red[kFewWaves * 16 * MB * 16 * RB];
+    constexpr int H = 8 * RB;
+    const int lane = threadIdx.x & 63;
+    const int64_t c0 = (int64_t)H * blockIdx.x, ld = p.k * in_bytes(IN);
+    const uint8_t *wrow[RB], *xrow[MB];
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+        const int r = 16 * b + (lane & 15);
+        wrow[b] = (const uint8_t *)(r < H ? p.w_gate : p.w_up) + min(c0 + r % H, p.n - 1) * ld;
+    }
+#pragma unroll
+    for (int b = 0; b < MB; ++b) xrow[b] = (const uint8_t *)p.x + min((int64_t)16 * b + (lane & 15), p.m - 1) * ld;
+    few_sums<IN, RB, MB, U>(red, wrow, xrow, (int)ld);
+    for (int i = threadIdx.x; i < H * (int)p.m; i += kFewThreads) {
+        const int ch = i % H, tk = i / H;
+        const int64_t c = c0 + ch, o = tk * p.n + c;
+        if (c >= p.n) continue;
+        float g = few_join<IN, RB, MB>(red, tk, ch), u = few_join<IN, RB, MB>(red, tk, H + ch);
+        if constexpr (IN == IN_I8) {
+            g = g * p.x_scale[tk] * p.gate_scale[c];
+            u = u * p.x_scale[tk] * p.up_scale[c];
+        }
+        store_one<DT>(p.h, o, act_value<ACT>(g) * u);
+        if constexpr (SAVE) {
+            store_one<DT>(p.g, o, g);
+            store_one<DT>(p.u, o, u);
+        }
+    }
+}
+
+template <int IN, int DT, int ACT, bool SAVE, int RB, int MB, int U>
+void go_few(const GluArgs &a, hipStream_t s)
+{
+    k_glu_few<IN, DT, ACT, SAVE, RB, MB, U><<<(unsigned)((a.n + 8 * RB - 1) / (8 * RB)), kFewThreads, 0, s>>>(a);
+}
+
 template <int IN, int DT, int ACT, bool SAVE, int MI, int NB, int NS, bool PF>
 void go(const GluArgs &a, hipStream_t s)
 {
@@ -103,7 +144,10 @@ void launch(const GluArgs &a, hipStream_t s)
 {
     with_act(a.act, [&](auto act) {
         constexpr int A = decltype(act)::value;
-        if ((a.m + 255) / 256 * ((a.n + 127) / 128) >= 128) go<IN, DT, A, SAVE, 4, 4, 2, true>(a, s);
+        if (a.m <= 16) go_few<IN, DT, A, SAVE, 1, 1, 4>(a, s);
+        else if (a.m <= 32) go_few<IN, DT, A, SAVE, 1, 2, 2>(a, s);
+        else if (a.m <= 64) go_few<IN, DT, A, SAVE, 2, 4, 2>(a, s);
+        else if ((a.m + 255) / 256 * ((a.n + 127) / 128) >= 128) go<IN, DT, A, SAVE, 4, 4, 2, true>(a, s);
         else go<IN, DT, A, SAVE, 2, 2, 4, false>(a, s);
     });
 }
