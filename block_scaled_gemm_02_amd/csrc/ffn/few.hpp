@@ -1,7 +1,7 @@
 // Products of a few tokens: the weights are read once and bound the time.
 //
-// A workgroup of 8 waves computes 16 RB weight rows (output channels) for up
-// to 16 MB tokens.  The waves split K: wave w takes the 128-byte pieces w,
+// A workgroup of 8 waves computes 16 weight rows (output channels) for up to
+// 16 MB tokens.  The waves split K: wave w takes the 128-byte pieces w,
 // w + 8, ... of every row, straight into registers in the layout of the 16x16
 // MFMAs (lane (r = l%16, g = l/16) holds 16 bytes of row r), U pieces ahead,
 // and the 8 partial sums are joined in LDS, in a fixed order.  So every
@@ -14,8 +14,6 @@
 
 namespace bsg {
 namespace ffn {
-
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 template <int IN>
 __device__ __forceinline__ f32x4 mfma16(const i32x4 &w, const i32x4 &x, const f32x4 &acc)
@@ -30,24 +28,23 @@ __device__ __forceinline__ f32x4 mfma16(const i32x4 &w, const i32x4 &x, const f3
 
 constexpr int kFewWaves = 8, kFewThreads = 64 * kFewWaves;
 
-// Sums over K of 16 RB weight rows against 16 MB tokens.  wrow: this lane's
-// weight row of block b at wrow[b]; xrow: its token of block b (a token past
-// the last one repeats it: its column is not stored).  The result is left in
-// red: partial w of (token, channel) at red[(w * 16 MB + token) * 16 RB + channel].
-template <int IN, int RB, int MB, int U>
-__device__ __forceinline__ void few_sums(float *red, const uint8_t *const (&wrow)[RB], const uint8_t *const (&xrow)[MB],
+// Sums over K of 16 weight rows against 16 MB tokens.  wrow: this lane's
+// weight row; xrow: its token of block b (a row or token past the last one
+// repeats it: it is not stored).  The result is left in red: partial w of
+// (token, channel) at red[(w * 16 MB + token) * 16 + channel].
+template <int IN, int MB, int U>
+__device__ __forceinline__ void few_sums(float *red, const uint8_t *wrow, const uint8_t *const (&xrow)[MB],
                                          int kbytes)
 {
     const int lane = threadIdx.x & 63, w = wave_id(), g = lane >> 4;
     struct Piece {
-        i32x4 w[RB][2], x[MB][2];
+        i32x4 w[2], x[MB][2];
     };
-    f32x4 acc[RB][MB] = {};
+    f32x4 acc[MB] = {};
     auto load = [&](Piece &p, int k) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int b = 0; b < RB; ++b) p.w[b][h] = *reinterpret_cast<const i32x4 *>(wrow[b] + k + 64 * h + 16 * g);
+            p.w[h] = *reinterpret_cast<const i32x4 *>(wrow + k + 64 * h + 16 * g);
 #pragma unroll
             for (int b = 0; b < MB; ++b) p.x[b][h] = *reinterpret_cast<const i32x4 *>(xrow[b] + k + 64 * h + 16 * g);
         }
@@ -56,9 +53,7 @@ __device__ __forceinline__ void few_sums(float *red, const uint8_t *const (&wrow
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int b = 0; b < RB; ++b)
-#pragma unroll
-                for (int t = 0; t < MB; ++t) acc[b][t] = mfma16<IN>(p.w[b][h], p.x[t][h], acc[b][t]);
+            for (int t = 0; t < MB; ++t) acc[t] = mfma16<IN>(p.w[h], p.x[t][h], acc[t]);
     };
     // whole pieces of this wave, U at a time, the next ones on their way
     const int full = kbytes / 128, mine = full > w ? (full - w + kFewWaves - 1) / kFewWaves : 0;
@@ -91,11 +86,8 @@ __device__ __forceinline__ void few_sums(float *red, const uint8_t *const (&wrow
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const bool in = k + 64 * h + 16 * g < kbytes;
-#pragma unroll
-            for (int b = 0; b < RB; ++b) {
-                p.w[b][h] = i32x4{0, 0, 0, 0};
-                if (in) p.w[b][h] = *reinterpret_cast<const i32x4 *>(wrow[b] + k + 64 * h + 16 * g);
-            }
+            p.w[h] = i32x4{0, 0, 0, 0};
+            if (in) p.w[h] = *reinterpret_cast<const i32x4 *>(wrow + k + 64 * h + 16 * g);
 #pragma unroll
             for (int b = 0; b < MB; ++b) {
                 p.x[b][h] = i32x4{0, 0, 0, 0};
@@ -105,19 +97,16 @@ __device__ __forceinline__ void few_sums(float *red, const uint8_t *const (&wrow
         mma(p);
     }
 #pragma unroll
-    for (int b = 0; b < RB; ++b)
-#pragma unroll
-        for (int t = 0; t < MB; ++t)
-            *reinterpret_cast<f32x4 *>(red + ((w * 16 * MB + 16 * t + (lane & 15)) * 16 * RB + 16 * b + 4 * g)) = acc[b][t];
+    for (int t = 0; t < MB; ++t) *reinterpret_cast<f32x4 *>(red + (w * 16 * MB + 16 * t + (lane & 15)) * 16 + 4 * g) = acc[t];
     __syncthreads();
 }
 
 // The joined sum of (token, channel), as the accumulator's type gives it.
-template <int IN, int RB, int MB>
+template <int IN, int MB>
 __device__ __forceinline__ float few_join(const float *red, int token, int channel)
 {
-    const float *p = red + token * 16 * RB + channel;
-    constexpr int S = 16 * MB * 16 * RB;
+    const float *p = red + token * 16 + channel;
+    constexpr int S = 16 * MB * 16;
     if constexpr (IN == IN_I8) {
         int s = 0;
 #pragma unroll

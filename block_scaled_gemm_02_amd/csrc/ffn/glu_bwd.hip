@@ -34,11 +34,9 @@ __global__ __launch_bounds__(256) void k_dact(const uint4 *dh, const uint4 *g, c
     d[r * 2 * n8 + n8 + c] = b;
 }
 
-template <int DT, int MI, int NB, int kStage, class Ptr>
-__device__ __forceinline__ void store16(f32x16 (&acc)[MI][NB], uint8_t *reg, int rows, int cols, uint32_t row_bytes,
-                                        int lane, Ptr &&dst)
+template <int DT, int MI, int NB, class Flush>
+__device__ __forceinline__ void store16(f32x16 (&acc)[MI][NB], uint8_t *reg, int lane, Flush &&flush)
 {
-    static_assert(32 * StageGeom<2, NB>::RBP <= kStage, "the staging fits the wave's part of the ring");
     static_for<MI>([&](auto ii) {
         constexpr int i = decltype(ii)::value;
         __builtin_amdgcn_sched_barrier(0);
@@ -47,112 +45,151 @@ __device__ __forceinline__ void store16(f32x16 (&acc)[MI][NB], uint8_t *reg, int
             constexpr int j = decltype(jj)::value, q = decltype(qq)::value;
             return make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
         });
-        dst(i, rows - 32 * i, 2 * cols);
+        flush(i);
     });
 }
 
 // dX: K runs over the n columns of dG against Wg, then of dU against Wu; each
-// part is padded to whole pairs with zeros.
-template <int IN, int MI, int NB, int NS, bool PF>
-__global__ __launch_bounds__(256, MI *NB == 16 ? 1 : 2) void k_dx(GluBwdArgs p, const uint8_t *d, int mt, int nt)
+// part is padded to whole pairs with zeros.  d: [dG | dU]; sums: the splits'.
+template <int IN, class S, bool SPLIT>
+__global__ __launch_bounds__(256, S::kWaves) void k_dx(GluBwdArgs p, const uint8_t *d, float *sums, int mt, int nt, int splits)
 {
-    typedef Tile<IN, true, false, MI, NB, NS, PF> T;
+    typedef typename S::template Of<IN, true, false> T;
+    constexpr int MI = S::MI, NB = S::NB;
     __shared__ __attribute__((aligned(16))) uint8_t ring[T::kLds];
-    const int lane = threadIdx.x & 63, w = wave_id(), wm = w >> 1, wn = w & 1;
-    const TileAt at = tile_at(blockIdx.x, mt, nt);
-    const int64_t m0 = (int64_t)T::TM * at.m, n0 = (int64_t)T::TN * at.n, ld = 4 * p.n, lw = 2 * p.k;
+    const int lane = threadIdx.x & 63, w = wave_id();
     const int np = pairs_of(2 * p.n);
+    const Split sp = split_of(SPLIT ? blockIdx.x % splits : 0, SPLIT ? splits : 1, 2 * np);
+    const TileAt at = SPLIT ? tile_split(blockIdx.x / splits, mt) : tile_at(blockIdx.x, mt, nt);
+    const int64_t m0 = (int64_t)S::TM * at.m, n0 = (int64_t)S::TN * at.n, ld = 4 * p.n, lw = 2 * p.k;
     typename T::LA la;
     typename T::LB lb;
-    const int64_t r = m0 + T::TM / 4 * w;
+    const int64_t r = m0 + S::TM / 4 * w;
     const uint8_t *const da = d + r * ld, *const wg = (const uint8_t *)p.w_gate + 2 * n0, *const wu = (const uint8_t *)p.w_up + 2 * n0;
     la.init_k(da, (p.m - r) * ld, ld, 2 * p.n, w, lane);
     lb.init_mn(wg, p.n * lw - 2 * n0, lw, p.k - n0, w, lane);
-    f32x16 acc[MI][NB];
-    T t;
-    t.run(acc, ring, la, lb, 2 * np, [&](int pair) {
-        const bool up = pair >= np;
+    auto seek = [&](int pair) {
+        const int q = sp.at(pair);
+        const bool up = q >= np;
         la.base = up ? da + 2 * p.n : da;
         // the last row's dU ends with the matrix
         la.r = make_rsrc_words(la.base, clamp_bytes((p.m - r) * ld - (up ? 2 * p.n : 0)));
         lb.base = up ? wu : wg;
-        la.seek(up ? pair - np : pair);
-        lb.seek(up ? pair - np : pair);
-    });
-    const int64_t r0 = m0 + 32 * MI * wm, c0 = n0 + 32 * NB * wn;
+        la.seek(up ? q - np : q);
+        lb.seek(up ? q - np : q);
+    };
+    f32x16 acc[MI][NB];
+    T t;
+    t.run(acc, ring, la, lb, sp.count, seek);
+    const int64_t r0 = m0 + 32 * MI * (w >> 1), c0 = n0 + 32 * NB * (w & 1);
     const int rows = (int)min((int64_t)32 * MI, p.m - r0), cols = (int)min((int64_t)32 * NB, p.k - c0);
     uint8_t *const reg = ring + w * T::kStage;
-    store16<dt_of(IN), MI, NB, T::kStage>(acc, reg, rows, cols, (uint32_t)lw, lane, [&](int i, int rv, int cb) {
-        flush_block<2, NB>(reg, (char *)p.dx + 2 * ((r0 + 32 * i) * p.k + c0), (uint32_t)lw, rv, cb, lane);
-    });
+    static_assert(32 * StageGeom<SPLIT ? 4 : 2, NB>::RBP <= T::kStage, "the staging fits the wave's part of the ring");
+    if constexpr (SPLIT) {
+        put_sums<NB, 0>(acc, reg, sums + (sp.index * p.m + r0) * p.k + c0, p.k, rows, cols, lane);
+    } else {
+        store16<dt_of(IN)>(acc, reg, lane, [&](int i) {
+            flush_block<2, NB>(reg, (char *)p.dx + 2 * ((r0 + 32 * i) * p.k + c0), (uint32_t)lw, rows - 32 * i, 2 * cols, lane);
+        });
+    }
 }
 
 // dWg (rows 0 .. n) and dWu (rows n .. 2n)
-template <int IN, int MI, int NB, int NS, bool PF>
-__global__ __launch_bounds__(256, MI *NB == 16 ? 1 : 2) void k_dw(GluBwdArgs p, const uint8_t *d, int mt, int nt)
+template <int IN, class S, bool SPLIT>
+__global__ __launch_bounds__(256, S::kWaves) void k_dw(GluBwdArgs p, const uint8_t *d, float *sums, int mt, int nt, int splits)
 {
-    typedef Tile<IN, false, false, MI, NB, NS, PF> T;
+    typedef typename S::template Of<IN, false, false> T;
+    constexpr int MI = S::MI, NB = S::NB;
     __shared__ __attribute__((aligned(16))) uint8_t ring[T::kLds];
-    const int lane = threadIdx.x & 63, w = wave_id(), wm = w >> 1, wn = w & 1;
-    const TileAt at = tile_at(blockIdx.x, mt, nt);
-    const int64_t m0 = (int64_t)T::TM * at.m, n0 = (int64_t)T::TN * at.n, ld = 4 * p.n, lx = 2 * p.k;
+    const int lane = threadIdx.x & 63, w = wave_id();
+    const Split sp = split_of(SPLIT ? blockIdx.x % splits : 0, SPLIT ? splits : 1, pairs_of(2 * p.m));
+    const TileAt at = SPLIT ? tile_split(blockIdx.x / splits, mt) : tile_at(blockIdx.x, mt, nt);
+    const int64_t m0 = (int64_t)S::TM * at.m, n0 = (int64_t)S::TN * at.n, ld = 4 * p.n, lx = 2 * p.k;
     typename T::LA la;
     typename T::LB lb;
     la.init_mn(d + 2 * m0, p.m * ld - 2 * m0, ld, 2 * p.n - m0, w, lane);
     lb.init_mn((const uint8_t *)p.x + 2 * n0, p.m * lx - 2 * n0, lx, p.k - n0, w, lane);
+    auto seek = [&](int pair) {
+        la.seek(sp.at(pair));
+        lb.seek(sp.at(pair));
+    };
     f32x16 acc[MI][NB];
     T t;
-    t.run(acc, ring, la, lb, pairs_of(2 * p.m), [&](int pair) {
-        la.seek(pair);
-        lb.seek(pair);
-    });
-    const int64_t r0 = m0 + 32 * MI * wm, c0 = n0 + 32 * NB * wn;
+    t.run(acc, ring, la, lb, sp.count, seek);
+    const int64_t r0 = m0 + 32 * MI * (w >> 1), c0 = n0 + 32 * NB * (w & 1);
     const int rows = (int)min((int64_t)32 * MI, 2 * p.n - r0), cols = (int)min((int64_t)32 * NB, p.k - c0);
     uint8_t *const reg = ring + w * T::kStage;
-    store16<dt_of(IN), MI, NB, T::kStage>(acc, reg, rows, cols, (uint32_t)lx, lane, [&](int i, int rv, int cb) {
-        // a 32-row block may straddle the two gradients
-        const int64_t row = r0 + 32 * i;
-        const int gate = (int)min((int64_t)32, max((int64_t)0, p.n - row));
-        flush_block<2, NB>(reg, (char *)p.dw_gate + 2 * (row * p.k + c0), (uint32_t)lx, min(gate, rv), cb, lane);
-        // (its rows of dWu start at staged row `gate`)
-        flush_block<2, NB>(reg + gate * StageGeom<2, NB>::RBP, (char *)p.dw_up + 2 * ((row + gate - p.n) * p.k + c0),
-                           (uint32_t)lx, min(32, rv) - gate, cb, lane);
-    });
+    // (a block's second flush may start at any of its rows)
+    static_assert(64 * StageGeom<2, NB>::RBP <= T::kStage && 32 * StageGeom<SPLIT ? 4 : 2, NB>::RBP <= T::kStage,
+                  "the staging fits the wave's part of the ring");
+    if constexpr (SPLIT) {
+        put_sums<NB, 0>(acc, reg, sums + (sp.index * 2 * p.n + r0) * p.k + c0, p.k, rows, cols, lane);
+    } else {
+        store16<dt_of(IN)>(acc, reg, lane, [&](int i) {
+            // a 32-row block may straddle the two gradients: its first `gate` rows are dWg's
+            const int64_t row = r0 + 32 * i;
+            const int rv = min(32, rows - 32 * i), gate = (int)min((int64_t)32, max((int64_t)0, p.n - row));
+            flush_block<2, NB>(reg, (char *)p.dw_gate + 2 * (row * p.k + c0), (uint32_t)lx, min(gate, rv), 2 * cols, lane);
+            flush_block<2, NB>(reg + gate * StageGeom<2, NB>::RBP, (char *)p.dw_up + 2 * ((row + gate - p.n) * p.k + c0),
+                               (uint32_t)lx, rv - gate, 2 * cols, lane);
+        });
+    }
 }
+
+// Joins the splits' sums of `count4` times four outputs; the first `first4`
+// go to out0, the others to out1.
+template <int DT>
+__global__ __launch_bounds__(256) void k_join(const float *sums, void *out0, void *out1, int64_t first4, int64_t count4, int splits)
+{
+    const int64_t i = 256ll * blockIdx.x + threadIdx.x;
+    if (i >= count4) return;
+    const float4 s = join4<IN_BF16>(sums + 4 * i, 4 * count4, splits);
+    if (i < first4) store4<DT>(out0, 4 * i, s);
+    else store4<DT>(out1, 4 * (i - first4), s);
+}
+
+Plan dx_plan(int64_t m, int64_t n, int64_t k) { return plan_of(m, k, 2 * ((2 * n + 127) / 128 * 128)); }
+Plan dw_plan(int64_t m, int64_t n, int64_t k) { return plan_of(2 * n, k, 2 * m); }
+int64_t d_bytes(int64_t m, int64_t n) { return (4 * m * n + 255) / 256 * 256; }
 
 }  // namespace
 
-int64_t workspace_gemm_glu_bwd(int64_t m, int64_t n, int64_t) { return (4 * m * n + 255) / 256 * 256; }
+int64_t workspace_gemm_glu_bwd(int64_t m, int64_t n, int64_t k)
+{
+    // dX and the weight gradients follow each other: their splits share the space
+    const Plan x = dx_plan(m, n, k), w = dw_plan(m, n, k);
+    const int64_t sx = x.splits > 1 ? 4 * m * k * x.splits : 0, sw = w.splits > 1 ? 8 * n * k * w.splits : 0;
+    return d_bytes(m, n) + (sx > sw ? sx : sw);
+}
 
 hipError_t launch_gemm_glu_bwd(const GluBwdArgs &a, hipStream_t s)
 {
     uint8_t *d = (uint8_t *)a.workspace;
-    const int64_t count = a.m * a.n / 8;
+    float *sums = (float *)(d + d_bytes(a.m, a.n));
+    auto blocks = [](int64_t items) { return (unsigned)((items + 255) / 256); };
     auto by_type = [&](auto in) {
         constexpr int I = decltype(in)::value;
-        if (count) {
+        if (const int64_t count = a.m * a.n / 8) {
             with_act(a.act, [&](auto act) {
-                k_dact<dt_of(I), decltype(act)::value><<<(unsigned)((count + 255) / 256), 256, 0, s>>>(
+                k_dact<dt_of(I), decltype(act)::value><<<blocks(count), 256, 0, s>>>(
                     (const uint4 *)a.dh, (const uint4 *)a.g, (const uint4 *)a.u, (uint4 *)d, count, (uint32_t)(a.n / 8));
             });
         }
-        auto go = [&](auto big, int64_t m, int64_t n, auto &&launch) {
-            constexpr int E = decltype(big)::value ? 256 : 128;
-            const int mt = (int)((m + E - 1) / E), nt = (int)((n + E - 1) / E);
-            launch((unsigned)mt * (unsigned)nt, mt, nt);
-        };
-        auto big = [](int64_t m, int64_t n) { return (m + 255) / 256 * ((n + 255) / 256) >= 128; };
         if (a.dx && a.m && a.k) {
-            if (big(a.m, a.k))
-                go(std::true_type{}, a.m, a.k, [&](unsigned g, int mt, int nt) { k_dx<I, 4, 4, 2, true><<<g, 256, 0, s>>>(a, d, mt, nt); });
-            else
-                go(std::false_type{}, a.m, a.k, [&](unsigned g, int mt, int nt) { k_dx<I, 2, 2, 4, false><<<g, 256, 0, s>>>(a, d, mt, nt); });
+            const Plan p = dx_plan(a.m, a.n, a.k);
+            with_shape(p, [&](auto shape, auto split) {
+                k_dx<I, decltype(shape), decltype(split)::value><<<p.grid(), 256, 0, s>>>(a, d, sums, p.mt, p.nt, p.splits);
+            });
+            const int64_t c = a.m * a.k / 4;
+            if (p.splits > 1) k_join<dt_of(I)><<<blocks(c), 256, 0, s>>>(sums, a.dx, nullptr, c, c, p.splits);
         }
         if (a.dw_gate && a.n && a.k) {
-            if (big(2 * a.n, a.k))
-                go(std::true_type{}, 2 * a.n, a.k, [&](unsigned g, int mt, int nt) { k_dw<I, 4, 4, 2, true><<<g, 256, 0, s>>>(a, d, mt, nt); });
-            else
-                go(std::false_type{}, 2 * a.n, a.k, [&](unsigned g, int mt, int nt) { k_dw<I, 2, 2, 4, false><<<g, 256, 0, s>>>(a, d, mt, nt); });
+            const Plan p = dw_plan(a.m, a.n, a.k);
+            with_shape(p, [&](auto shape, auto split) {
+                k_dw<I, decltype(shape), decltype(split)::value><<<p.grid(), 256, 0, s>>>(a, d, sums, p.mt, p.nt, p.splits);
+            });
+            const int64_t c = a.n * a.k / 4;
+            if (p.splits > 1) k_join<dt_of(I)><<<blocks(2 * c), 256, 0, s>>>(sums, a.dw_gate, a.dw_up, c, 2 * c, p.splits);
         }
     };
     if (a.dtype == DT_F16) by_type(std::integral_constant<int, IN_F16>{});

@@ -5,115 +5,149 @@ namespace bsg {
 namespace ffn {
 namespace {
 
-// A tile holds (32 NB) columns of H: the B panel of a wave's quadrant is half
-// gate rows, half up rows, so that a lane's gate and up accumulators belong
-// to the same elements of H.
-// DT: the type of H (and of G and U, stored if SAVE).
-template <int IN, int DT, int ACT, bool SAVE, int MI, int NB, int NS, bool PF>
-__global__ __launch_bounds__(256, MI *NB == 16 ? 1 : 2) void k_glu(GluArgs p, int mt, int nt)
+// Scales, gates and stores four columns of row r from column c on.
+template <int IN, int DT, int ACT, bool SAVE>
+__device__ __forceinline__ void finish4(const GluArgs &p, int64_t r, int64_t c, float4 g, float4 u)
 {
-    typedef Tile<IN, true, true, MI, NB, NS, PF> T;
-    constexpr int HW = NB / 2, ES = in_bytes(IN);
+    if constexpr (IN == IN_I8) {
+        const float rs = p.x_scale[r], *const gs = p.gate_scale + c, *const us = p.up_scale + c;
+        g = make_float4(g.x * rs * gs[0], g.y * rs * gs[1], g.z * rs * gs[2], g.w * rs * gs[3]);
+        u = make_float4(u.x * rs * us[0], u.y * rs * us[1], u.z * rs * us[2], u.w * rs * us[3]);
+    }
+    const int64_t o = r * p.n + c;
+    store4<DT>(p.h, o, make_float4(act_value<ACT>(g.x) * u.x, act_value<ACT>(g.y) * u.y, act_value<ACT>(g.z) * u.z,
+                                   act_value<ACT>(g.w) * u.w));
+    if constexpr (SAVE) {
+        store4<DT>(p.g, o, g);
+        store4<DT>(p.u, o, u);
+    }
+}
+
+// A tile holds TN / 2 columns of H: of the B panel's rows for each wave's
+// quadrant half are gate rows and half the up rows of the same columns, so
+// that a lane's gate and up sums belong to the same elements of H.  DT: the type of H (and of G and U, stored if SAVE).
+template <int IN, int DT, int ACT, bool SAVE, class S, bool SPLIT>
+__global__ __launch_bounds__(256, S::kWaves) void k_glu(GluArgs p, int mt, int nt, int splits)
+{
+    typedef typename S::template Of<IN, true, true> T;
+    constexpr int MI = S::MI, NB = S::NB, ES = in_bytes(IN);
     __shared__ __attribute__((aligned(16))) uint8_t ring[T::kLds];
-    const int lane = threadIdx.x & 63, w = wave_id(), wm = w >> 1, wn = w & 1;
-    const TileAt at = tile_at(blockIdx.x, mt, nt);
-    const int64_t ld = p.k * ES, m0 = (int64_t)T::TM * at.m, h0 = (int64_t)(T::TN / 2) * at.n;
+    const int lane = threadIdx.x & 63, w = wave_id();
+    const int64_t ld = p.k * ES;
+    const Split sp = split_of(SPLIT ? blockIdx.x % splits : 0, SPLIT ? splits : 1, pairs_of(ld));
+    const TileAt at = SPLIT ? tile_split(blockIdx.x / splits, mt) : tile_at(blockIdx.x, mt, nt);
+    const int64_t m0 = (int64_t)S::TM * at.m, h0 = (int64_t)(S::TN / 2) * at.n;
     typename T::LA la;
     typename T::LB lb;
     {
-        const int64_t r = m0 + T::TM / 4 * w, c = h0 + 16 * NB * (w >> 1);
+        const int64_t r = m0 + S::TM / 4 * w, c = h0 + S::TN / 4 * (w >> 1);
         la.init_k((const uint8_t *)p.x + r * ld, (p.m - r) * ld, ld, ld, w, lane);
         lb.init_k((const uint8_t *)(w & 1 ? p.w_up : p.w_gate) + c * ld, (p.n - c) * ld, ld, ld, w, lane);
     }
-    const int64_t r0 = m0 + 32 * MI * wm, c0 = h0 + 16 * NB * wn;
-    const int rows = (int)min((int64_t)32 * MI, p.m - r0), cols = (int)min((int64_t)32 * HW, p.n - c0);
-    // scales, in registers over the K loop: a row's for each block, and of
-    // the wave's 32 HW columns lane l holds gate (l) and up scale
+    auto seek = [&](int pair) {
+        la.seek(sp.at(pair));
+        lb.seek(sp.at(pair));
+    };
+    f32x16 acc[MI][NB];
+    T t;
+    constexpr int HW = NB / 2, HC = 32 * HW;
+    const int64_t r0 = m0 + 32 * MI * (w >> 1), c0 = h0 + HC * (w & 1);
+    const int rows = (int)min((int64_t)32 * MI, p.m - r0), cols = (int)min((int64_t)HC, p.n - c0);
+    // scales, in registers over the K loop: a row's for each block, and of the
+    // wave's HC <= 64 columns lane l holds gate (l) and up scale
     float rs[MI], gs = 0.0f, us = 0.0f;
-    if constexpr (IN == IN_I8) {
+    if constexpr (IN == IN_I8 && !SPLIT) {
 #pragma unroll
         for (int i = 0; i < MI; ++i) rs[i] = 32 * i + (lane & 31) < rows ? p.x_scale[r0 + 32 * i + (lane & 31)] : 0.0f;
-        if (lane < min(cols, 32 * HW)) {
+        if (lane < cols) {
             gs = p.gate_scale[c0 + lane];
             us = p.up_scale[c0 + lane];
         }
     }
-    f32x16 acc[MI][NB];
-    T t;
-    t.run(acc, ring, la, lb, pairs_of(ld), [&](int pair) {
-        la.seek(pair);
-        lb.seek(pair);
-    });
-
+    t.run(acc, ring, la, lb, sp.count, seek);
     uint8_t *const reg = ring + w * T::kStage;
-    constexpr int kReg = 32 * StageGeom<2, HW>::RBP;
-    float *const cs = reinterpret_cast<float *>(reg + kReg);   // gate, then up scales of the columns
-    if constexpr (IN == IN_I8) {
-        cs[lane < 32 * HW ? lane : 64 * HW] = gs;
-        cs[lane < 32 * HW ? 32 * HW + lane : 64 * HW] = us;
-    }
-    const uint32_t row_bytes = (uint32_t)(2 * p.n);
-    static_for<MI>([&](auto ii) {
-        constexpr int i = decltype(ii)::value;
-        __builtin_amdgcn_sched_barrier(0);
-        pin(acc[i]);
-        // the unscaled pre-activations of one quad
-        auto quad = [&](auto blk, auto qq) {
-            constexpr int b = decltype(blk)::value, q = decltype(qq)::value;
-            float4 x = make_float4(acc[i][b][4 * q], acc[i][b][4 * q + 1], acc[i][b][4 * q + 2], acc[i][b][4 * q + 3]);
-            if constexpr (IN == IN_I8) {
-                const float4 s = *reinterpret_cast<const float4 *>(cs + 32 * b + 8 * q + 4 * (lane >> 5));
-                x.x = (float)__float_as_int(x.x) * rs[i] * s.x;
-                x.y = (float)__float_as_int(x.y) * rs[i] * s.y;
-                x.z = (float)__float_as_int(x.z) * rs[i] * s.z;
-                x.w = (float)__float_as_int(x.w) * rs[i] * s.w;
+    if constexpr (SPLIT) {
+        // sums of the gate columns [0, n) and the up columns [n, 2n)
+        float *const dst = (float *)p.workspace + (sp.index * p.m + r0) * 2 * p.n + c0;
+        put_sums<HW, 0>(acc, reg, dst, 2 * p.n, rows, cols, lane);
+        put_sums<HW, HW>(acc, reg, dst + p.n, 2 * p.n, rows, cols, lane);
+    } else {
+        constexpr int kReg = 32 * StageGeom<2, HW>::RBP;
+        static_assert(3 * kReg <= T::kStage && kReg + 512 <= T::kStage, "the staging fits the wave's part of the ring");
+        float *const cs = reinterpret_cast<float *>(reg + kReg);   // gate, then up scales of the columns (integers)
+        if constexpr (IN == IN_I8) {
+            if (lane < HC) {
+                cs[lane] = gs;
+                cs[HC + lane] = us;
             }
-            return x;
-        };
-        auto up = [&](auto j, auto q) { return quad(std::integral_constant<int, decltype(j)::value + HW>{}, q); };
-        auto h = [&](auto j, auto q) {
-            const float4 g = quad(j, q), u = up(j, q);
-            return make_float4(act_value<ACT>(g.x) * u.x, act_value<ACT>(g.y) * u.y, act_value<ACT>(g.z) * u.z,
-                               act_value<ACT>(g.w) * u.w);
-        };
-        const int64_t o = 2 * ((r0 + 32 * i) * p.n + c0);
-        stage_block<DT, HW>(reg, lane, h);
-        if constexpr (SAVE) {
-            stage_block<DT, HW>(reg + kReg, lane, quad);
-            stage_block<DT, HW>(reg + 2 * kReg, lane, up);
         }
-        flush_block<2, HW>(reg, (char *)p.h + o, row_bytes, rows - 32 * i, 2 * cols, lane);
-        if constexpr (SAVE) {
-            flush_block<2, HW>(reg + kReg, (char *)p.g + o, row_bytes, rows - 32 * i, 2 * cols, lane);
-            flush_block<2, HW>(reg + 2 * kReg, (char *)p.u + o, row_bytes, rows - 32 * i, 2 * cols, lane);
-        }
-    });
-    static_assert(3 * kReg + 512 <= T::kStage, "the staging fits the wave's part of the ring");
+        const uint32_t row_bytes = (uint32_t)(2 * p.n);
+        static_for<MI>([&](auto ii) {
+            constexpr int i = decltype(ii)::value;
+            __builtin_amdgcn_sched_barrier(0);
+            pin(acc[i]);
+            // four gate (block column b) or up (b + HW) values of the lane's row
+            auto quad = [&](auto blk, auto qq) {
+                constexpr int b = decltype(blk)::value, q = decltype(qq)::value;
+                float4 x = make_float4(acc[i][b][4 * q], acc[i][b][4 * q + 1], acc[i][b][4 * q + 2], acc[i][b][4 * q + 3]);
+                if constexpr (IN == IN_I8) {
+                    const float4 s = *reinterpret_cast<const float4 *>(cs + 32 * b + 8 * q + 4 * (lane >> 5));
+                    x.x = (float)__float_as_int(x.x) * rs[i] * s.x;
+                    x.y = (float)__float_as_int(x.y) * rs[i] * s.y;
+                    x.z = (float)__float_as_int(x.z) * rs[i] * s.z;
+                    x.w = (float)__float_as_int(x.w) * rs[i] * s.w;
+                }
+                return x;
+            };
+            auto up = [&](auto j, auto q) { return quad(std::integral_constant<int, decltype(j)::value + HW>{}, q); };
+            auto h = [&](auto j, auto q) {
+                const float4 g = quad(j, q), u = up(j, q);
+                return make_float4(act_value<ACT>(g.x) * u.x, act_value<ACT>(g.y) * u.y, act_value<ACT>(g.z) * u.z,
+                                   act_value<ACT>(g.w) * u.w);
+            };
+            const int64_t o = 2 * ((r0 + 32 * i) * p.n + c0);
+            stage_block<DT, HW>(reg, lane, h);
+            if constexpr (SAVE) {
+                stage_block<DT, HW>(reg + kReg, lane, quad);
+                stage_block<DT, HW>(reg + 2 * kReg, lane, up);
+            }
+            flush_block<2, HW>(reg, (char *)p.h + o, row_bytes, rows - 32 * i, 2 * cols, lane);
+            if constexpr (SAVE) {
+                flush_block<2, HW>(reg + kReg, (char *)p.g + o, row_bytes, rows - 32 * i, 2 * cols, lane);
+                flush_block<2, HW>(reg + 2 * kReg, (char *)p.u + o, row_bytes, rows - 32 * i, 2 * cols, lane);
+            }
+        });
+    }
 }
 
-// A few tokens: of a workgroup's 16 RB weight rows the first half are gate
-// rows and the second the up rows of the same channels.
-template <int IN, int DT, int ACT, bool SAVE, int RB, int MB, int U>
+// Joins the splits' sums: four columns a thread.
+template <int IN, int DT, int ACT, bool SAVE>
+__global__ __launch_bounds__(256) void k_glu_join(GluArgs p, int splits)
+{
+    const int64_t i = 256ll * blockIdx.x + threadIdx.x, n4 = p.n / 4;
+    if (i >= p.m * n4) return;
+    const int64_t r = i / n4, c = i % n4 * 4;
+    const float *const src = (const float *)p.workspace + r * 2 * p.n + c;
+    finish4<IN, DT, ACT, SAVE>(p, r, c, join4<IN>(src, 2 * p.m * p.n, splits),
+                               join4<IN>(src + p.n, 2 * p.m * p.n, splits));
+}
+
+// A few tokens: of a workgroup's 16 weight rows 8 are gate rows and 8 the up
+// rows of the same channels.
+template <int IN, int DT, int ACT, bool SAVE, int MB, int U>
 __global__ __launch_bounds__(kFewThreads) void k_glu_few(GluArgs p)
 {
-    __shared__ __attribute__((aligned(16))) float red[kFewWaves * 16 * MB * 16 * RB];
-    constexpr int H = 8 * RB;
+    __shared__ __attribute__((aligned(16))) float red[kFewWaves * 16 * MB * 16];
     const int lane = threadIdx.x & 63;
-    const int64_t c0 = (int64_t)H * blockIdx.x, ld = p.k * in_bytes(IN);
-    const uint8_t *wrow[RB], *xrow[MB];
-#pragma unroll
-    for (int b = 0; b < RB; ++b) {
-        const int r = 16 * b + (lane & 15);
-        wrow[b] = (const uint8_t *)(r < H ? p.w_gate : p.w_up) + min(c0 + r % H, p.n - 1) * ld;
-    }
+    const int64_t c0 = 8ll * blockIdx.x, ld = p.k * in_bytes(IN);
+    const uint8_t *const wrow = (const uint8_t *)(lane & 8 ? p.w_up : p.w_gate) + (c0 + (lane & 7)) * ld, *xrow[MB];
 #pragma unroll
     for (int b = 0; b < MB; ++b) xrow[b] = (const uint8_t *)p.x + min((int64_t)16 * b + (lane & 15), p.m - 1) * ld;
-    few_sums<IN, RB, MB, U>(red, wrow, xrow, (int)ld);
-    for (int i = threadIdx.x; i < H * (int)p.m; i += kFewThreads) {
-        const int ch = i % H, tk = i / H;
+    few_sums<IN, MB, U>(red, wrow, xrow, (int)ld);
+    for (int i = threadIdx.x; i < 8 * (int)p.m; i += kFewThreads) {
+        const int ch = i % 8, tk = i / 8;
         const int64_t c = c0 + ch, o = tk * p.n + c;
-        if (c >= p.n) continue;
-        float g = few_join<IN, RB, MB>(red, tk, ch), u = few_join<IN, RB, MB>(red, tk, H + ch);
+        float g = few_join<IN, MB>(red, tk, ch), u = few_join<IN, MB>(red, tk, 8 + ch);
         if constexpr (IN == IN_I8) {
             g = g * p.x_scale[tk] * p.gate_scale[c];
             u = u * p.x_scale[tk] * p.up_scale[c];
@@ -126,17 +160,10 @@ __global__ __launch_bounds__(kFewThreads) void k_glu_few(GluArgs p)
     }
 }
 
-template <int IN, int DT, int ACT, bool SAVE, int RB, int MB, int U>
+template <int IN, int DT, int ACT, bool SAVE, int MB, int U>
 void go_few(const GluArgs &a, hipStream_t s)
 {
-    k_glu_few<IN, DT, ACT, SAVE, RB, MB, U><<<(unsigned)((a.n + 8 * RB - 1) / (8 * RB)), kFewThreads, 0, s>>>(a);
-}
-
-template <int IN, int DT, int ACT, bool SAVE, int MI, int NB, int NS, bool PF>
-void go(const GluArgs &a, hipStream_t s)
-{
-    const int mt = (int)((a.m + 64 * MI - 1) / (64 * MI)), nt = (int)((a.n + 32 * NB - 1) / (32 * NB));
-    k_glu<IN, DT, ACT, SAVE, MI, NB, NS, PF><<<(unsigned)mt * (unsigned)nt, 256, 0, s>>>(a, mt, nt);
+    k_glu_few<IN, DT, ACT, SAVE, MB, U><<<(unsigned)(a.n / 8), kFewThreads, 0, s>>>(a);
 }
 
 template <int IN, int DT, bool SAVE>
@@ -144,17 +171,27 @@ void launch(const GluArgs &a, hipStream_t s)
 {
     with_act(a.act, [&](auto act) {
         constexpr int A = decltype(act)::value;
-        if (a.m <= 16) go_few<IN, DT, A, SAVE, 1, 1, 4>(a, s);
-        else if (a.m <= 32) go_few<IN, DT, A, SAVE, 1, 2, 2>(a, s);
-        else if (a.m <= 64) go_few<IN, DT, A, SAVE, 2, 4, 2>(a, s);
-        else if ((a.m + 255) / 256 * ((a.n + 127) / 128) >= 128) go<IN, DT, A, SAVE, 4, 4, 2, true>(a, s);
-        else go<IN, DT, A, SAVE, 2, 2, 4, false>(a, s);
+        if (few_is_cheaper(a.m, 2 * a.n, a.k * in_bytes(IN))) {
+            if (a.m <= 16) return go_few<IN, DT, A, SAVE, 1, 2>(a, s);
+            if (a.m <= 32) return go_few<IN, DT, A, SAVE, 2, 2>(a, s);
+            return go_few<IN, DT, A, SAVE, 4, 1>(a, s);
+        }
+        const Plan p = plan_of(a.m, 2 * a.n, a.k * in_bytes(IN));
+        with_shape(p, [&](auto shape, auto split) {
+            k_glu<IN, DT, A, SAVE, decltype(shape), decltype(split)::value><<<p.grid(), 256, 0, s>>>(a, p.mt, p.nt, p.splits);
+        });
+        if (p.splits > 1) k_glu_join<IN, DT, A, SAVE><<<(unsigned)((a.m * a.n / 4 + 255) / 256), 256, 0, s>>>(a, p.splits);
     });
 }
 
 }  // namespace
 
-int64_t workspace_gemm_glu(int64_t, int64_t, int64_t, bool) { return 0; }
+int64_t workspace_gemm_glu(int64_t m, int64_t n, int64_t k, bool in_i8)
+{
+    if (few_is_cheaper(m, 2 * n, in_i8 ? k : 2 * k)) return 0;
+    const Plan p = plan_of(m, 2 * n, in_i8 ? k : 2 * k);
+    return p.splits > 1 ? 8 * m * n * p.splits : 0;
+}
 
 hipError_t launch_gemm_glu(const GluArgs &a, hipStream_t s)
 {

@@ -1,0 +1,82 @@
+// How a product is cut into workgroups: host code, shared by the launches and
+// the workspace sizes.
+#pragma once
+#include <stdint.h>
+
+#include <algorithm>
+
+namespace bsg {
+namespace ffn {
+
+struct Plan {
+    int shape;      // 0: Big (256 x 256), 1: Mid (128 x 128), 2: Small (64 x 128)
+    int splits;     // parts of K (Mid only; 1: whole)
+    int mt, nt;     // tiles
+    double us;      // the estimate
+    unsigned grid() const { return (unsigned)mt * (unsigned)nt * (unsigned)splits; }
+};
+
+// The cheapest plan of a rows x cols product over kbytes of K by an estimate
+// in microseconds, from times measured on the card (256 compute units):
+//   * a pair of 128 bytes of K takes a Big tile 1.03 us while at most 128 tiles
+//     are at work (2048 cycles of MFMA) and 1.5 us at 256 (the clock falls
+//     under the power limit); a Mid tile 0.35 and 0.485 us, a Small one 0.28
+//     and 0.31 us, whatever its MFMAs: the loads bound those;
+//   * launch, first loads and epilogue: 6, 5.5 and 4.5 us, and 4, 3 and 1.5 us
+//     for each further round of 256 tiles;
+//   * the operands come from memory at 4.9 TB/s;
+//   * splitting K (few tiles, long K) costs 3.5 us for the second kernel and
+//     the partial sums' way to memory and back at 2.5 TB/s of them.
+// Measured against it (us, Big / Mid / Small / Mid split in 4): 67 x 4096,
+// K 7168 int8: 63.3 / 23.7 / 19.9 / 13.3; 300 x 1000, K 1504 int8: 20.5 / 11.0
+// / 7.9 / 10.3; 512 x 4096, K 4096 int8: 39.8 / 17.1 / 14.2 / 25.1; 1000 x
+// 4096, K 4096 bf16: 70.7 / 38.1 / 44.3; 2048 x 8192, K 4096 int8: 62.3 / 82.3
+// / 95.2.
+inline Plan plan_of(int64_t rows, int64_t cols, int64_t kbytes)
+{
+    struct Cost {
+        int tm, tn;
+        double fixed, round, pair, pair_all;
+    };
+    static constexpr Cost kCost[3] = {{256, 256, 6.0, 4.0, 1.03, 1.5}, {128, 128, 5.5, 3.0, 0.35, 0.485}, {64, 128, 4.5, 1.5, 0.28, 0.31}};
+    const int64_t pairs = kbytes > 128 ? (kbytes + 127) / 128 : 1;
+    Plan best{};
+    double least = 0;
+    for (int s = 0; s < 3; ++s) {
+        const Cost &c = kCost[s];
+        const int64_t mt = (rows + c.tm - 1) / c.tm, nt = (cols + c.tn - 1) / c.tn;
+        // a split keeps at least four pairs, and splits never make more workgroups than two rounds
+        for (int n = 1; n == 1 || (s == 1 && n <= 8 && pairs >= 4 * n && mt * nt * n <= 512); ++n) {
+            const int64_t tiles = mt * nt * n, full = tiles / 256, rest = tiles % 256;
+            const double part = rest > 128 ? c.pair + (c.pair_all - c.pair) * (double)(rest - 128) / 128 : c.pair;
+            double t = c.fixed + (double)(full + (rest > 0) - 1) * c.round +
+                       (double)((pairs + n - 1) / n) * ((double)full * c.pair_all + (rest ? part : 0));
+            t = std::max(t, c.fixed + (double)(rows + cols) * (double)kbytes / 4.9e6);
+            if (n > 1) t += 3.5 + (double)rows * (double)cols * n * 4 / 2.5e6;
+            if (!best.splits || t < least) {
+                best = {s, n, (int)mt, (int)nt, t};
+                least = t;
+            }
+        }
+    }
+    return best;
+}
+
+// The same estimate for the kernel of a few tokens (up to 64), cols weight
+// rows in all: the weights at 5.2 TB/s, and the tokens' rows, which every
+// workgroup of 16 weight rows reads from the L2 at 45 bytes a nanosecond and
+// compute unit (the first six hide behind the weights).  Measured, few / tiles
+// (us): 16 tokens of 4096 x 7168 int8 8.9 / 12; 32 tokens 12.1 / 12.1; gated
+// bf16 2048 x 7168, 16 tokens 15.1 / 18, 32 tokens 21.0 / 18; 8192 x 4096, 16
+// tokens 35.4 / 33.7; 512 x 512, 32 tokens 3.8 / 6.8.
+inline bool few_is_cheaper(int64_t tokens, int64_t cols, int64_t kbytes)
+{
+    if (tokens > 64) return false;
+    const double rounds = (double)((cols + 4095) / 4096);
+    const double t = 2.5 + (double)cols * (double)kbytes / 5.2e6 +
+                     rounds * (double)std::max<int64_t>(0, tokens - 6) * (double)kbytes / 45000.0;
+    return t <= plan_of(tokens, cols, kbytes).us;
+}
+
+}  // namespace ffn
+}  // namespace bsg

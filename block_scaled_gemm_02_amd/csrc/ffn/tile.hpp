@@ -20,14 +20,18 @@
 // c ^ s(r), s(r) = (r%8) ^ ((r/8)%2), so that the 16 lanes that a 128-bit
 // read serves at once cover all 64 banks.
 // mn-major panel (16-bit; rows of M or N at each K): K row kk at (2 T) kk, its
-// 64-byte block b at b ^ (kk%4); the transposing read (ds_read_b64_tr_b16)
-// of a half wave takes 64 bytes from each of 4 consecutive K rows, which the
-// exchange puts on different banks.
+// 64-byte block b at b ^ x(kk); the transposing read (ds_read_b64_tr_b16) of a
+// half wave takes 64 bytes from each of 4 consecutive K rows, which x puts on
+// different banks: kk%4, or (kk%4)/2 where a row has two blocks only (T = 64)
+// and its neighbour the other half of the banks.
 #pragma once
 #include "act.hpp"
+#include "plan.hpp"
 
 namespace bsg {
 namespace ffn {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 enum In : int { IN_BF16 = 0, IN_F16 = 1, IN_I8 = 2 };
 constexpr int in_bytes(int in) { return in == IN_I8 ? 1 : 2; }
@@ -51,6 +55,9 @@ __device__ __forceinline__ int pairs_of(int64_t kbytes) { return kbytes > 128 ? 
 
 // Readable bytes as a buffer resource takes them.
 __device__ __forceinline__ uint32_t clamp_bytes(int64_t b) { return b <= 0 ? 0u : (b < 0x7FFFFFFF ? (uint32_t)b : 0x7FFFFFFFu); }
+
+template <int T>
+__device__ __forceinline__ uint32_t mn_swizzle(uint32_t kk) { return T == 64 ? (kk >> 1) & 1 : kk & 3; }
 
 // One wave's share of the loads of a T-row panel: T/32 loads of 1 KB a pair.
 // k-major: rows T/4 w ...  of the panel, base at the first of them, `bytes`
@@ -86,7 +93,7 @@ struct Loader {
 #pragma unroll
         for (int q = 0; q < L; ++q) {
             const uint32_t p = 1024u * (L * w + q) + 16u * (uint32_t)lane, kk = p / (2 * T), o = p % (2 * T);
-            const uint32_t col = o ^ (64u * (kk & 3));
+            const uint32_t col = o ^ (64u * mn_swizzle<T>(kk));
             v[q] = col < valid ? kk * (uint32_t)ld + col : kOOB;
         }
         constexpr uint32_t LPR = T / 64;       // lines of a K row
@@ -132,7 +139,7 @@ struct Reader {
             const uint32_t G = (uint32_t)lane >> 4, s = (uint32_t)lane & 15, kk = 8u * (G >> 1) + (s >> 2);
 #pragma unroll
             for (int c = 0; c < C; ++c)
-                off[c] = kk * (2u * T) + 64u * (((uint32_t)row0 / 32u + c) ^ (kk & 3)) + 32u * (G & 1) + 8u * (s & 3);
+                off[c] = kk * (2u * T) + 64u * (((uint32_t)row0 / 32u + c) ^ mn_swizzle<T>(kk)) + 32u * (G & 1) + 8u * (s & 3);
         }
     }
     // Read Q of the step in half H of a pair.
@@ -268,6 +275,72 @@ struct Tile {
     }
 };
 
+// The sum of `parts` partial sums of four columns, `stride` floats apart, the
+// first at p; integers are added as integers.
+// Four at a time, so that their latencies overlap.
+template <int IN>
+__device__ __forceinline__ float4 join4(const float *p, int64_t stride, int parts)
+{
+    typedef std::conditional_t<IN == IN_I8, i32x4, f32x4> V;
+    auto at = [&](int i) { return *reinterpret_cast<const V *>(p + i * stride); };
+    V s = at(0);
+    int i = 1;
+    for (; i + 4 <= parts; i += 4) {
+        const V a = at(i), b = at(i + 1), c = at(i + 2), d = at(i + 3);
+        s = s + a + b + c + d;
+    }
+    for (; i < parts; ++i) s = s + at(i);
+    return make_float4((float)s[0], (float)s[1], (float)s[2], (float)s[3]);
+}
+template <int DT>
+__device__ __forceinline__ void store4(void *p, int64_t i, float4 v)
+{
+    *reinterpret_cast<typename Quad<es_of<DT>()>::T *>((char *)p + i * es_of<DT>()) = pack_quad<DT>(v.x, v.y, v.z, v.w);
+}
+
+// The tile shapes: Big for products with enough 256 x 256 tiles, the others
+// with more and smaller ones, whose rings hold more pairs.  Below Big the
+// loads bound the time, not the matrix cores: a CU's direct-to-LDS loads reach
+// about 50 bytes a cycle, 32 KB (Mid) or 24 KB (Small) a pair for 512 or 256
+// cycles of MFMA.  (Letting the four waves divide a pair's K instead of the
+// tile, so that no fragment is read from LDS twice, gained nothing for that
+// reason and its joining of the four sums cost 2 us.)
+template <int MI_, int NB_, int NS_, bool PF_>
+struct Shape {
+    static constexpr int MI = MI_, NB = NB_, TM = 64 * MI, TN = 64 * NB;
+    static constexpr int kWaves = MI * NB == 16 ? 1 : 2;     // waves a SIMD that the registers allow
+    template <int IN, bool AK, bool BK>
+    using Of = Tile<IN, AK, BK, MI, NB, NS_, PF_>;
+};
+typedef Shape<4, 4, 2, true> Big;
+typedef Shape<2, 2, 4, false> Mid;
+typedef Shape<1, 2, 3, false> Small;
+
+// K divided over workgroups, where a product has fewer tiles than the card
+// has compute units: split s of `splits` sums the pairs [first, first + count)
+// of all `pairs` and leaves the raw sums in the workspace, for a second kernel
+// to join in the order of the splits.
+struct Split {
+    int index, first, count, pairs;
+    // the p-th pair of the split, or one past all of K, which reads nothing
+    __device__ __forceinline__ int at(int p) const { return p < count ? first + p : pairs; }
+};
+__device__ __forceinline__ Split split_of(int index, int splits, int pairs)
+{
+    const int a = (int)((int64_t)pairs * index / splits), b = (int)((int64_t)pairs * (index + 1) / splits);
+    return {index, a, b - a, pairs};
+}
+
+// f(shape, std::bool_constant<split>)
+template <class F>
+void with_shape(const Plan &p, F &&f)
+{
+    if (p.shape == 0) f(Big{}, std::false_type{});
+    else if (p.shape == 2) f(Small{}, std::false_type{});
+    else if (p.splits == 1) f(Mid{}, std::false_type{});
+    else f(Mid{}, std::true_type{});
+}
+
 // Order of tiles: workgroup b runs on XCD b % 8, 32 tiles of an XCD at a time
 // (one workgroup a CU).  XCDs take runs of 32 tiles in turn; tiles go in
 // squares of 16 x 16, a square in strips of 4 rows, so that an XCD's run is
@@ -287,6 +360,10 @@ __device__ __forceinline__ TileAt tile_at(uint32_t b, uint32_t mt, uint32_t nt)
     const uint32_t st = r2 / (G * cols), r3 = r2 % (G * cols), g = min(G, rows - st * G);
     return {(int)(sq * Q + st * G + r3 % g), (int)(c * Q + r3 / g)};
 }
+
+// Tiles of a split product: rows fastest, so that the workgroups that read
+// the same columns' weights start together.
+__device__ __forceinline__ TileAt tile_split(uint32_t b, uint32_t mt) { return {(int)(b % mt), (int)(b / mt)}; }
 
 // Holds a row of accumulator blocks in their AGPRs up to here: the compiler
 // otherwise reads all 256 at the end of the K loop and spills the fragments.
@@ -316,7 +393,7 @@ __device__ __forceinline__ void stage_block(uint8_t *reg, int lane, F &&value)
         });
     });
 }
-template <int ES, int W>
+template <int ES, int W, bool STREAM = true>
 __device__ __forceinline__ void flush_block(const uint8_t *reg, void *dst, uint32_t row_bytes, int rows, int col_bytes,
                                             int lane)
 {
@@ -329,14 +406,31 @@ __device__ __forceinline__ void flush_block(const uint8_t *reg, void *dst, uint3
     const uint32_t n = (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)max(0, min(rows, 32)) * row_bytes));
     const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(udst, (short)0, (int)n, 0x00020000);
     const uint32_t voff = cb < col_bytes ? (uint32_t)lr * row_bytes + (uint32_t)cb : kOOB;
-    // streamed past the L2 (nt) where a wave writes whole 128-byte lines: it
-    // is left to the operand panels
-    constexpr int kNT = G::RB % 128 == 0 ? 2 : 0;
+    // outputs are streamed past the L2 (nt), which is left to the operand
+    // panels, where a wave writes whole 128-byte lines
+    constexpr int kNT = STREAM && G::RB % 128 == 0 ? 2 : 0;
 #pragma unroll
     for (int k = 0; k < G::NK; ++k) {
         const i32x4 v = *reinterpret_cast<const i32x4 *>(reg + (lr + k * G::RPI) * G::RBP + cb);
         __builtin_amdgcn_raw_buffer_store_b128(v, rs, voff + (uint32_t)(k * G::RPI) * row_bytes, 0, kNT);
     }
+}
+
+// The raw sums of W accumulator blocks from block column J0 on, to dst (row
+// stride ld floats): a split's part of the workspace.
+template <int W, int J0, int MI, int NB>
+__device__ __forceinline__ void put_sums(f32x16 (&acc)[MI][NB], uint8_t *reg, float *dst, int64_t ld, int rows, int cols, int lane)
+{
+    static_for<MI>([&](auto ii) {
+        constexpr int i = decltype(ii)::value;
+        __builtin_amdgcn_sched_barrier(0);
+        pin(acc[i]);
+        stage_block<DT_F32, W>(reg, lane, [&](auto jj, auto qq) {
+            constexpr int j = J0 + decltype(jj)::value, q = decltype(qq)::value;
+            return make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+        });
+        flush_block<4, W, false>(reg, dst + 32 * i * ld, (uint32_t)(4 * ld), rows - 32 * i, 4 * cols, lane);
+    });
 }
 
 }  // namespace ffn

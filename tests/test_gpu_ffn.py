@@ -47,7 +47,9 @@ def scratch(name, m, n, k):
 # k, long k with few rows, k of one piece
 SIZES = [(1, 8, 16), (1, 256, 4112), (3, 264, 528), (16, 136, 80), (17, 520, 1040), (33, 64, 4096), (63, 248, 272),
          (64, 256, 64), (65, 1032, 336), (127, 72, 144), (129, 392, 1056), (200, 2048, 32), (257, 640, 400),
-         (300, 264, 2064), (513, 1288, 192), (700, 24, 6016), (1030, 520, 112)]
+         (300, 264, 2064), (513, 1288, 192), (700, 24, 6016), (1030, 520, 112),
+         # K in parts (few tiles, long K), and the largest tiles
+         (100, 264, 9008), (72, 1032, 4528), (2305, 4104, 80), (4100, 2056, 1040)]
 
 
 # ---------------------------------------------------------------------------
@@ -189,7 +191,8 @@ def test_gemm_glu(i, size):
 
 
 @pytest.mark.parametrize("dt", [BF, HF])
-@pytest.mark.parametrize("m,n,k", [(1, 520, 1032), (15, 264, 520), (70, 136, 4104), (131, 1032, 200), (600, 392, 1000)])
+@pytest.mark.parametrize("m,n,k", [(1, 520, 1032), (15, 264, 520), (40, 72, 264), (70, 136, 4104), (131, 1032, 200),
+                                   (600, 392, 1000), (2500, 4104, 264)])
 def test_gemm_glu_small_integers_are_exact(m, n, k, dt):
     """Small integers: every fp32 sum is exact in any order, so G, U and
     ReLU(G) * U are the 64-bit values rounded once.  A column or a piece of K
@@ -264,7 +267,9 @@ def test_gemm_glu_i8(i, size):
 
 # ---------------------------------------------------------------------------
 BWD = [(1, 8, 8), (7, 64, 24), (64, 72, 136), (129, 264, 200), (200, 520, 64), (257, 136, 1032), (515, 1288, 264),
-       (1000, 256, 520), (2050, 40, 72)]
+       (1000, 256, 520), (2050, 40, 72),
+       # dX with K in parts, the weight gradients with K in parts, the largest tiles for either
+       (100, 4504, 264), (9000, 136, 264), (4100, 520, 4104), (200, 4104, 2056)]
 
 
 def run_bwd(dh, x, wg, wu, g, u, kind, want=(True, True)):
@@ -302,7 +307,7 @@ def test_gemm_glu_bwd(i, size):
         assert torch.equal(only_w[1], got[1]) and torch.equal(only_w[2], got[2]) and bool((only_w[0] == 77).all())
 
 
-@pytest.mark.parametrize("m,n,k", [(40, 136, 264), (300, 264, 520), (1001, 72, 136)])
+@pytest.mark.parametrize("m,n,k", [(40, 136, 264), (300, 264, 520), (1001, 72, 136), (4099, 264, 4104)])
 def test_gemm_glu_bwd_small_integers_are_exact(m, n, k):
     """ReLU, small integers: dG, dU and every sum are exact."""
     say("gemm_glu_bwd exact", m, n, k)
