@@ -168,7 +168,7 @@ def _grouped_common_need(padded_offsets, alpha, prob, m, num_experts):
 
 def _stream(stream):
     if stream is None:      # torch.cuda.current_stream().cuda_stream, without making a Stream object (2.8 us)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -435,16 +435,30 @@ def workspace_bytes(name, m, n, k) -> int:
 _TORCH_OF = {F32: torch.float32, F16: torch.float16, BF16: torch.bfloat16}
 
 
-def _needs(*specs):
-    """_need for several (tensor, name, bytes, torch dtype): a call for one
-    token takes a few microseconds, and one pass of quick checks takes one;
-    whatever does not pass them goes to _need, which says what is wrong."""
-    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+def _code(dtype, t) -> int:
+    """dtype_code of a dtype argument, or of the tensor t if it is None."""
+    x = t.dtype if dtype is None and isinstance(t, torch.Tensor) else dtype
+    c = _TORCH_DT.get(x)
+    return dtype_code(x) if c is None else c
+
+
+def _addresses(*specs):
+    """The addresses of several (tensor, name, bytes, torch dtype), checked as
+    _need does.  A call for one token takes a few microseconds, and this one
+    pass of quick checks takes one; what does not pass them goes to _need,
+    which says what is wrong."""
+    dev, out = None, []
     for t, name, nbytes, dt in specs:
         if t is None or type(t) is int:
+            out.append(t)
             continue
-        if t.get_device() != dev or t.dtype is not dt or t.nbytes < nbytes or not t.is_contiguous():
+        d = t.get_device()
+        if dev is None and d >= 0:
+            dev = torch._C._cuda_getDevice()
+        if d != dev or t.dtype is not dt or t.nbytes < nbytes or not t.is_contiguous():
             _need(t, name, nbytes, dt)
+        out.append(t.data_ptr())
+    return out
 
 
 def _act(act) -> int:
@@ -459,16 +473,16 @@ def _ws(workspace, name, m, n, k):
         return None, 0
     if isinstance(workspace, int):
         return workspace, lib().bsg_workspace_bytes(_WS_OPS[name], m, n, k)
-    _needs((workspace, "workspace", 0, workspace.dtype))
-    return workspace.data_ptr(), workspace.nbytes
+    return _addresses((workspace, "workspace", 0, workspace.dtype))[0], workspace.nbytes
 
 
 def quant_i8(x, q, scale, m, k, x_dtype=None, stream=None, validate_only=False):
     """Rows of x (m, k) -> 8-bit integers q and one fp32 scale a row (see
     include/bsg.h).  x_dtype: torch.float32 / float16 / bfloat16, from x if None."""
-    xd = dtype_code(x_dtype if x_dtype is not None else x)
-    _needs((x, "x", _out_bytes(xd, m * k), _TORCH_OF.get(xd)), (q, "q", m * k, torch.int8), (scale, "scale", 4 * m, torch.float32))
-    args = [_ptr(x), _ptr(q), _ptr(scale), m, k, xd]
+    xd = _code(x_dtype, x)
+    args = _addresses((x, "x", _out_bytes(xd, m * k), _TORCH_OF.get(xd)), (q, "q", m * k, torch.int8),
+                      (scale, "scale", 4 * m, torch.float32))
+    args += (m, k, xd)
     if validate_only:
         return lib().bsg_validate_quant_i8(*args)
     _check(lib().quant_i8(*args, _stream(stream)))
@@ -478,13 +492,12 @@ def gemm_i8(a, b, a_scale, b_scale, bias, c, m, n, k, bias_dtype=None, c_dtype=N
             stream=None, validate_only=False):
     """c = (a b^T) * a_scale[:, None] * b_scale + bias from 8-bit integers
     (see include/bsg.h).  bias may be None."""
-    cd = dtype_code(c_dtype if c_dtype is not None else c)
-    bd = dtype_code(bias_dtype if bias_dtype is not None else (bias if bias is not None else torch.float32))
-    _needs((a, "a", m * k, torch.int8), (b, "b", n * k, torch.int8), (a_scale, "a_scale", 4 * m, torch.float32),
-           (b_scale, "b_scale", 4 * n, torch.float32), (bias, "bias", _out_bytes(bd, n), _TORCH_OF.get(bd)),
-           (c, "c", _out_bytes(cd, m * n), _TORCH_OF.get(cd)))
-    args = [_ptr(a), _ptr(b), _ptr(a_scale), _ptr(b_scale), _ptr(bias), _ptr(c),
-            *_ws(workspace, "gemm_i8", m, n, k), m, n, k, bd, cd]
+    cd = _code(c_dtype, c)
+    bd = F32 if bias is None else _code(bias_dtype, bias)
+    args = _addresses((a, "a", m * k, torch.int8), (b, "b", n * k, torch.int8), (a_scale, "a_scale", 4 * m, torch.float32),
+                      (b_scale, "b_scale", 4 * n, torch.float32), (bias, "bias", _out_bytes(bd, n), _TORCH_OF.get(bd)),
+                      (c, "c", _out_bytes(cd, m * n), _TORCH_OF.get(cd)))
+    args += (*_ws(workspace, "gemm_i8", m, n, k), m, n, k, bd, cd)
     if validate_only:
         return lib().bsg_validate_gemm_i8(*args)
     _check(lib().gemm_i8(*args, _stream(stream)))
@@ -495,12 +508,11 @@ def gemm_glu(x, w_gate, w_up, h, g, u, m, n, k, act="silu", dtype=None, workspac
     """h = act(x w_gate^T) * (x w_up^T), and the two products in g and u
     unless they are None (see include/bsg.h).  act: "silu", "gelu_tanh" or
     "relu".  dtype: torch.float16 / bfloat16 of every tensor, from x if None."""
-    dt = dtype_code(dtype if dtype is not None else x)
+    dt = _code(dtype, x)
     mn, nk, td = _out_bytes(dt, m * n), _out_bytes(dt, n * k), _TORCH_OF.get(dt)
-    _needs((x, "x", _out_bytes(dt, m * k), td), (w_gate, "w_gate", nk, td), (w_up, "w_up", nk, td), (h, "h", mn, td),
-           (g, "g", mn, td), (u, "u", mn, td))
-    args = [_ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(h), _ptr(g), _ptr(u),
-            *_ws(workspace, "gemm_glu", m, n, k), m, n, k, dt, _act(act)]
+    args = _addresses((x, "x", _out_bytes(dt, m * k), td), (w_gate, "w_gate", nk, td), (w_up, "w_up", nk, td),
+                      (h, "h", mn, td), (g, "g", mn, td), (u, "u", mn, td))
+    args += (*_ws(workspace, "gemm_glu", m, n, k), m, n, k, dt, _act(act))
     if validate_only:
         return lib().bsg_validate_gemm_glu(*args)
     _check(lib().gemm_glu(*args, _stream(stream)))
@@ -509,13 +521,12 @@ def gemm_glu(x, w_gate, w_up, h, g, u, m, n, k, act="silu", dtype=None, workspac
 def gemm_glu_i8(a, w_gate, w_up, a_scale, gate_scale, up_scale, h, m, n, k, act="silu", h_dtype=None,
                 workspace=None, stream=None, validate_only=False):
     """gemm_glu from 8-bit integers and their scales (see include/bsg.h)."""
-    dt = dtype_code(h_dtype if h_dtype is not None else h)
+    dt = _code(h_dtype, h)
     i8, f32 = torch.int8, torch.float32
-    _needs((a, "a", m * k, i8), (w_gate, "w_gate", n * k, i8), (w_up, "w_up", n * k, i8), (a_scale, "a_scale", 4 * m, f32),
-           (gate_scale, "gate_scale", 4 * n, f32), (up_scale, "up_scale", 4 * n, f32),
-           (h, "h", _out_bytes(dt, m * n), _TORCH_OF.get(dt)))
-    args = [_ptr(a), _ptr(w_gate), _ptr(w_up), _ptr(a_scale), _ptr(gate_scale), _ptr(up_scale), _ptr(h),
-            *_ws(workspace, "gemm_glu_i8", m, n, k), m, n, k, dt, _act(act)]
+    args = _addresses((a, "a", m * k, i8), (w_gate, "w_gate", n * k, i8), (w_up, "w_up", n * k, i8),
+                      (a_scale, "a_scale", 4 * m, f32), (gate_scale, "gate_scale", 4 * n, f32),
+                      (up_scale, "up_scale", 4 * n, f32), (h, "h", _out_bytes(dt, m * n), _TORCH_OF.get(dt)))
+    args += (*_ws(workspace, "gemm_glu_i8", m, n, k), m, n, k, dt, _act(act))
     if validate_only:
         return lib().bsg_validate_gemm_glu_i8(*args)
     _check(lib().gemm_glu_i8(*args, _stream(stream)))
@@ -525,13 +536,13 @@ def gemm_glu_bwd(dh, x, w_gate, w_up, g, u, dx, dw_gate, dw_up, m, n, k, act="si
                  workspace=None, stream=None, validate_only=False):
     """Gradients of gemm_glu from dh and the saved g and u (see include/bsg.h).
     dx, or dw_gate and dw_up together, may be None."""
-    dt = dtype_code(dtype if dtype is not None else dh)
+    dt = _code(dtype, dh)
     mn, mk, nk = _out_bytes(dt, m * n), _out_bytes(dt, m * k), _out_bytes(dt, n * k)
     td = _TORCH_OF.get(dt)
-    _needs((dh, "dh", mn, td), (x, "x", mk, td), (w_gate, "w_gate", nk, td), (w_up, "w_up", nk, td), (g, "g", mn, td),
-           (u, "u", mn, td), (dx, "dx", mk, td), (dw_gate, "dw_gate", nk, td), (dw_up, "dw_up", nk, td))
-    args = [_ptr(dh), _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(g), _ptr(u), _ptr(dx), _ptr(dw_gate), _ptr(dw_up),
-            *_ws(workspace, "gemm_glu_bwd", m, n, k), m, n, k, dt, _act(act)]
+    args = _addresses((dh, "dh", mn, td), (x, "x", mk, td), (w_gate, "w_gate", nk, td), (w_up, "w_up", nk, td),
+                      (g, "g", mn, td), (u, "u", mn, td), (dx, "dx", mk, td), (dw_gate, "dw_gate", nk, td),
+                      (dw_up, "dw_up", nk, td))
+    args += (*_ws(workspace, "gemm_glu_bwd", m, n, k), m, n, k, dt, _act(act))
     if validate_only:
         return lib().bsg_validate_gemm_glu_bwd(*args)
     _check(lib().gemm_glu_bwd(*args, _stream(stream)))
