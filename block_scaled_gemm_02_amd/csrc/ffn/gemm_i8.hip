@@ -34,8 +34,8 @@ __global__ __launch_bounds__(256, S::kWaves) void k_i8(I8Args p, int mt, int nt,
     constexpr int MI = S::MI, NB = S::NB;
     __shared__ __attribute__((aligned(16))) uint8_t ring[T::kLds];
     const int lane = threadIdx.x & 63, w = wave_id();
-    const Split sp = split_of(SPLIT ? blockIdx.x % splits : 0, SPLIT ? splits : 1, pairs_of(p.k));
-    const TileAt at = SPLIT ? tile_split(blockIdx.x / splits, mt) : tile_at(blockIdx.x, mt, nt);
+    const auto [at, part] = tile_of_block<SPLIT>(blockIdx.x, mt, nt, splits);
+    const Split sp = split_of(part, SPLIT ? splits : 1, pairs_of(p.k));
     const int64_t ld = p.k, m0 = (int64_t)S::TM * at.m, n0 = (int64_t)S::TN * at.n;
     typename T::LA la;
     typename T::LB lb;

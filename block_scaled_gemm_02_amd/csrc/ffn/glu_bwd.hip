@@ -59,8 +59,8 @@ __global__ __launch_bounds__(256, S::kWaves) void k_dx(GluBwdArgs p, const uint8
     __shared__ __attribute__((aligned(16))) uint8_t ring[T::kLds];
     const int lane = threadIdx.x & 63, w = wave_id();
     const int np = pairs_of(2 * p.n);
-    const Split sp = split_of(SPLIT ? blockIdx.x % splits : 0, SPLIT ? splits : 1, 2 * np);
-    const TileAt at = SPLIT ? tile_split(blockIdx.x / splits, mt) : tile_at(blockIdx.x, mt, nt);
+    const auto [at, part] = tile_of_block<SPLIT>(blockIdx.x, mt, nt, splits);
+    const Split sp = split_of(part, SPLIT ? splits : 1, 2 * np);
     const int64_t m0 = (int64_t)S::TM * at.m, n0 = (int64_t)S::TN * at.n, ld = 4 * p.n, lw = 2 * p.k;
     typename T::LA la;
     typename T::LB lb;
@@ -102,8 +102,8 @@ __global__ __launch_bounds__(256, S::kWaves) void k_dw(GluBwdArgs p, const uint8
     constexpr int MI = S::MI, NB = S::NB;
     __shared__ __attribute__((aligned(16))) uint8_t ring[T::kLds];
     const int lane = threadIdx.x & 63, w = wave_id();
-    const Split sp = split_of(SPLIT ? blockIdx.x % splits : 0, SPLIT ? splits : 1, pairs_of(2 * p.m));
-    const TileAt at = SPLIT ? tile_split(blockIdx.x / splits, mt) : tile_at(blockIdx.x, mt, nt);
+    const auto [at, part] = tile_of_block<SPLIT>(blockIdx.x, mt, nt, splits);
+    const Split sp = split_of(part, SPLIT ? splits : 1, pairs_of(2 * p.m));
     const int64_t m0 = (int64_t)S::TM * at.m, n0 = (int64_t)S::TN * at.n, ld = 4 * p.n, lx = 2 * p.k;
     typename T::LA la;
     typename T::LB lb;

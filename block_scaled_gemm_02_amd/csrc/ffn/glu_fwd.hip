@@ -34,8 +34,8 @@ __global__ __launch_bounds__(256, S::kWaves) void k_glu(GluArgs p, int mt, int n
     __shared__ __attribute__((aligned(16))) uint8_t ring[T::kLds];
     const int lane = threadIdx.x & 63, w = wave_id();
     const int64_t ld = p.k * ES;
-    const Split sp = split_of(SPLIT ? blockIdx.x % splits : 0, SPLIT ? splits : 1, pairs_of(ld));
-    const TileAt at = SPLIT ? tile_split(blockIdx.x / splits, mt) : tile_at(blockIdx.x, mt, nt);
+    const auto [at, part] = tile_of_block<SPLIT>(blockIdx.x, mt, nt, splits);
+    const Split sp = split_of(part, SPLIT ? splits : 1, pairs_of(ld));
     const int64_t m0 = (int64_t)S::TM * at.m, h0 = (int64_t)(S::TN / 2) * at.n;
     typename T::LA la;
     typename T::LB lb;

@@ -341,29 +341,48 @@ void with_shape(const Plan &p, F &&f)
     else f(Mid{}, std::true_type{});
 }
 
-// Order of tiles: workgroup b runs on XCD b % 8, 32 tiles of an XCD at a time
-// (one workgroup a CU).  XCDs take runs of 32 tiles in turn; tiles go in
-// squares of 16 x 16, a square in strips of 4 rows, so that an XCD's run is
-// 4 x 8 tiles, whose 12 panels its L2 streams once, and the 8 runs that are
-// at work together are a square, whose 32 panels come from HBM once.
+// Order of workgroups: b runs on XCD b % 8, and each XCD has an L2 of its own.
+// The sequence is cut into rounds of 256 (a workgroup a CU), and each round
+// into one run an XCD, so that neighbours in the sequence share an L2.
+__device__ __forceinline__ uint32_t xcd_run(uint32_t b, uint32_t total)
+{
+    const uint32_t first = b / 256 * 256, round = min(256u, total - first), x = b % 8;
+    return first + x * (round / 8) + min(x, round % 8) + (b - first) / 8;
+}
+
 struct TileAt {
     int m, n;
 };
+// Tiles in squares of 16 x 16, a square in strips of 4 rows: an XCD's run is 4
+// x 8 tiles, whose 12 panels its L2 streams once, and a round is a square,
+// whose 32 panels come from memory once.
 __device__ __forceinline__ TileAt tile_at(uint32_t b, uint32_t mt, uint32_t nt)
 {
-    constexpr uint32_t R = 256, Q = 16, G = 4;
-    const uint32_t tiles = mt * nt;
-    uint32_t s = b;
-    if (b < tiles - tiles % R) s = b / R * R + b % 8 * 32 + b % R / 8;
+    constexpr uint32_t Q = 16, G = 4;
+    const uint32_t s = xcd_run(b, mt * nt);
     const uint32_t sq = s / (Q * nt), r = s % (Q * nt), rows = min(Q, mt - sq * Q);
     const uint32_t c = r / (rows * Q), r2 = r % (rows * Q), cols = min(Q, nt - c * Q);
     const uint32_t st = r2 / (G * cols), r3 = r2 % (G * cols), g = min(G, rows - st * G);
     return {(int)(sq * Q + st * G + r3 % g), (int)(c * Q + r3 / g)};
 }
 
-// Tiles of a split product: rows fastest, so that the workgroups that read
-// the same columns' weights start together.
-__device__ __forceinline__ TileAt tile_split(uint32_t b, uint32_t mt) { return {(int)(b % mt), (int)(b / mt)}; }
+// A split product: rows fastest, then splits, so that the workgroups that
+// read the same piece of the columns' weights share an L2.
+struct SplitTile {
+    TileAt at;
+    int split;
+};
+__device__ __forceinline__ SplitTile split_tile(uint32_t b, uint32_t mt, uint32_t nt, uint32_t splits)
+{
+    const uint32_t s = xcd_run(b, mt * nt * splits);
+    return {{(int)(s % mt), (int)(s / (mt * splits))}, (int)(s / mt % splits)};
+}
+template <bool SPLIT>
+__device__ __forceinline__ SplitTile tile_of_block(uint32_t b, uint32_t mt, uint32_t nt, uint32_t splits)
+{
+    if constexpr (SPLIT) return split_tile(b, mt, nt, splits);
+    else return {tile_at(b, mt, nt), 0};
+}
 
 // Holds a row of accumulator blocks in their AGPRs up to here: the compiler
 // otherwise reads all 256 at the end of the K loop and spills the fragments.
