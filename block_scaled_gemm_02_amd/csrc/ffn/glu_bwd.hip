@@ -1,9 +1,10 @@
 // gemm_glu_bwd: dX = dG Wg + dU Wu, dWg = dG^T X, dWu = dU^T X, with
 // dG = dH * U * act'(G) and dU = dH * act(G).
 //
-// Three launches: the element-wise pass writes [dG | dU] as one (m, 2n)
-// matrix; dX contracts it with the weights as they lie (their K rows are n);
-// both weight gradients are one product of 2n rows contracted over the tokens.
+// The element-wise pass writes [dG | dU] as one (m, 2n) matrix.  dX contracts
+// it with the weights as they lie (their K rows are n); both weight gradients
+// are one product of 2n rows contracted over the tokens.  The two products do
+// not depend on each other and go out as one launch where that is cheaper.
 #include "tile.hpp"
 
 namespace bsg {
@@ -52,14 +53,14 @@ __device__ __forceinline__ void store16(f32x16 (&acc)[MI][NB], uint8_t *reg, int
 // dX: K runs over the n columns of dG against Wg, then of dU against Wu; each
 // part is padded to whole pairs with zeros.  d: [dG | dU]; sums: the splits'.
 template <int IN, class S, bool SPLIT>
-__global__ __launch_bounds__(256, S::kWaves) void k_dx(GluBwdArgs p, const uint8_t *d, float *sums, int mt, int nt, int splits)
+__device__ __forceinline__ void dx_tile(const GluBwdArgs &p, const uint8_t *d, float *sums, int mt, int nt, int splits,
+                                        uint32_t block, uint8_t *ring)
 {
     typedef typename S::template Of<IN, true, false> T;
     constexpr int MI = S::MI, NB = S::NB;
-    __shared__ __attribute__((aligned(16))) uint8_t ring[T::kLds];
     const int lane = threadIdx.x & 63, w = wave_id();
     const int np = pairs_of(2 * p.n);
-    const auto [at, part] = tile_of_block<SPLIT>(blockIdx.x, mt, nt, splits);
+    const auto [at, part] = tile_of_block<SPLIT>(block, mt, nt, splits);
     const Split sp = split_of(part, SPLIT ? splits : 1, 2 * np);
     const int64_t m0 = (int64_t)S::TM * at.m, n0 = (int64_t)S::TN * at.n, ld = 4 * p.n, lw = 2 * p.k;
     typename T::LA la;
@@ -96,13 +97,13 @@ __global__ __launch_bounds__(256, S::kWaves) void k_dx(GluBwdArgs p, const uint8
 
 // dWg (rows 0 .. n) and dWu (rows n .. 2n)
 template <int IN, class S, bool SPLIT>
-__global__ __launch_bounds__(256, S::kWaves) void k_dw(GluBwdArgs p, const uint8_t *d, float *sums, int mt, int nt, int splits)
+__device__ __forceinline__ void dw_tile(const GluBwdArgs &p, const uint8_t *d, float *sums, int mt, int nt, int splits,
+                                        uint32_t block, uint8_t *ring)
 {
     typedef typename S::template Of<IN, false, false> T;
     constexpr int MI = S::MI, NB = S::NB;
-    __shared__ __attribute__((aligned(16))) uint8_t ring[T::kLds];
     const int lane = threadIdx.x & 63, w = wave_id();
-    const auto [at, part] = tile_of_block<SPLIT>(blockIdx.x, mt, nt, splits);
+    const auto [at, part] = tile_of_block<SPLIT>(block, mt, nt, splits);
     const Split sp = split_of(part, SPLIT ? splits : 1, pairs_of(2 * p.m));
     const int64_t m0 = (int64_t)S::TM * at.m, n0 = (int64_t)S::TN * at.n, ld = 4 * p.n, lx = 2 * p.k;
     typename T::LA la;
@@ -136,6 +137,29 @@ __global__ __launch_bounds__(256, S::kWaves) void k_dw(GluBwdArgs p, const uint8
     }
 }
 
+template <int IN, class S, bool SPLIT>
+__global__ __launch_bounds__(256, S::kWaves) void k_dx(GluBwdArgs p, const uint8_t *d, float *sums, int mt, int nt, int splits)
+{
+    __shared__ __attribute__((aligned(16))) uint8_t ring[S::template Of<IN, true, false>::kLds];
+    dx_tile<IN, S, SPLIT>(p, d, sums, mt, nt, splits, blockIdx.x, ring);
+}
+template <int IN, class S, bool SPLIT>
+__global__ __launch_bounds__(256, S::kWaves) void k_dw(GluBwdArgs p, const uint8_t *d, float *sums, int mt, int nt, int splits)
+{
+    __shared__ __attribute__((aligned(16))) uint8_t ring[S::template Of<IN, false, false>::kLds];
+    dw_tile<IN, S, SPLIT>(p, d, sums, mt, nt, splits, blockIdx.x, ring);
+}
+// Both: the tiles with the longer K first (x_first), so that short ones end the launch.
+template <int IN, class S>
+__global__ __launch_bounds__(256, S::kWaves) void k_dxw(GluBwdArgs p, const uint8_t *d, int xm, int xn, int wm, int wn, int x_first)
+{
+    static_assert(S::template Of<IN, true, false>::kLds == S::template Of<IN, false, false>::kLds, "one ring for both");
+    __shared__ __attribute__((aligned(16))) uint8_t ring[S::template Of<IN, true, false>::kLds];
+    const uint32_t first = x_first ? xm * xn : wm * wn, b = blockIdx.x;
+    if ((b < first) == (x_first != 0)) dx_tile<IN, S, false>(p, d, nullptr, xm, xn, 1, b < first ? b : b - first, ring);
+    else dw_tile<IN, S, false>(p, d, nullptr, wm, wn, 1, b < first ? b : b - first, ring);
+}
+
 // Joins the splits' sums of `count4` times four outputs; the first `first4`
 // go to out0, the others to out1.
 template <int DT>
@@ -148,8 +172,10 @@ __global__ __launch_bounds__(256) void k_join(const float *sums, void *out0, voi
     else store4<DT>(out1, 4 * (i - first4), s);
 }
 
-Plan dx_plan(int64_t m, int64_t n, int64_t k) { return plan_of(m, k, 2 * ((2 * n + 127) / 128 * 128)); }
-Plan dw_plan(int64_t m, int64_t n, int64_t k) { return plan_of(2 * n, k, 2 * m); }
+PlanPair plans(int64_t m, int64_t n, int64_t k)
+{
+    return plan_pair(m, k, 2 * ((2 * n + 127) / 128 * 128), 2 * n, k, 2 * m);
+}
 int64_t d_bytes(int64_t m, int64_t n) { return (4 * m * n + 255) / 256 * 256; }
 
 }  // namespace
@@ -157,7 +183,7 @@ int64_t d_bytes(int64_t m, int64_t n) { return (4 * m * n + 255) / 256 * 256; }
 int64_t workspace_gemm_glu_bwd(int64_t m, int64_t n, int64_t k)
 {
     // dX and the weight gradients follow each other: their splits share the space
-    const Plan x = dx_plan(m, n, k), w = dw_plan(m, n, k);
+    const auto [x, w, together] = plans(m, n, k);
     const int64_t sx = x.splits > 1 ? 4 * m * k * x.splits : 0, sw = w.splits > 1 ? 8 * n * k * w.splits : 0;
     return d_bytes(m, n) + (sx > sw ? sx : sw);
 }
@@ -175,21 +201,27 @@ hipError_t launch_gemm_glu_bwd(const GluBwdArgs &a, hipStream_t s)
                     (const uint4 *)a.dh, (const uint4 *)a.g, (const uint4 *)a.u, (uint4 *)d, count, (uint32_t)(a.n / 8));
             });
         }
-        if (a.dx && a.m && a.k) {
-            const Plan p = dx_plan(a.m, a.n, a.k);
-            with_shape(p, [&](auto shape, auto split) {
-                k_dx<I, decltype(shape), decltype(split)::value><<<p.grid(), 256, 0, s>>>(a, d, sums, p.mt, p.nt, p.splits);
+        const auto [px, pw, together] = plans(a.m, a.n, a.k);
+        const bool x = a.dx && a.m && a.k, w = a.dw_gate && a.n && a.k;
+        if (x && w && together) {
+            with_shape(px, [&, &px = px, &pw = pw](auto shape, auto) {
+                k_dxw<I, decltype(shape)><<<px.grid() + pw.grid(), 256, 0, s>>>(a, d, px.mt, px.nt, pw.mt, pw.nt, 2 * a.n >= a.m);
+            });
+            return;
+        }
+        if (x) {
+            with_shape(px, [&, &px = px](auto shape, auto split) {
+                k_dx<I, decltype(shape), decltype(split)::value><<<px.grid(), 256, 0, s>>>(a, d, sums, px.mt, px.nt, px.splits);
             });
             const int64_t c = a.m * a.k / 4;
-            if (p.splits > 1) k_join<dt_of(I)><<<blocks(c), 256, 0, s>>>(sums, a.dx, nullptr, c, c, p.splits);
+            if (px.splits > 1) k_join<dt_of(I)><<<blocks(c), 256, 0, s>>>(sums, a.dx, nullptr, c, c, px.splits);
         }
-        if (a.dw_gate && a.n && a.k) {
-            const Plan p = dw_plan(a.m, a.n, a.k);
-            with_shape(p, [&](auto shape, auto split) {
-                k_dw<I, decltype(shape), decltype(split)::value><<<p.grid(), 256, 0, s>>>(a, d, sums, p.mt, p.nt, p.splits);
+        if (w) {
+            with_shape(pw, [&, &pw = pw](auto shape, auto split) {
+                k_dw<I, decltype(shape), decltype(split)::value><<<pw.grid(), 256, 0, s>>>(a, d, sums, pw.mt, pw.nt, pw.splits);
             });
             const int64_t c = a.n * a.k / 4;
-            if (p.splits > 1) k_join<dt_of(I)><<<blocks(2 * c), 256, 0, s>>>(sums, a.dw_gate, a.dw_up, c, 2 * c, p.splits);
+            if (pw.splits > 1) k_join<dt_of(I)><<<blocks(2 * c), 256, 0, s>>>(sums, a.dw_gate, a.dw_up, c, 2 * c, pw.splits);
         }
     };
     if (a.dtype == DT_F16) by_type(std::integral_constant<int, IN_F16>{});

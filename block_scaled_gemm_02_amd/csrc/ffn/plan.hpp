@@ -32,31 +32,69 @@ struct Plan {
 // / 7.9 / 10.3; 512 x 4096, K 4096 int8: 39.8 / 17.1 / 14.2 / 25.1; 1000 x
 // 4096, K 4096 bf16: 70.7 / 38.1 / 44.3; 2048 x 8192, K 4096 int8: 62.3 / 82.3
 // / 95.2.
+struct ShapeCost {
+    int tm, tn;
+    double fixed, round, pair, pair_all;
+};
+static constexpr ShapeCost kShapeCost[3] = {
+    {256, 256, 6.0, 4.0, 1.03, 1.5}, {128, 128, 5.5, 3.0, 0.35, 0.485}, {64, 128, 4.5, 1.5, 0.28, 0.31}};
+
+inline int64_t pairs_in(int64_t kbytes) { return kbytes > 128 ? (kbytes + 127) / 128 : 1; }
+
+inline Plan plan_with(int shape, int splits, int64_t rows, int64_t cols, int64_t kbytes)
+{
+    const ShapeCost &c = kShapeCost[shape];
+    const int64_t mt = (rows + c.tm - 1) / c.tm, nt = (cols + c.tn - 1) / c.tn;
+    const int64_t tiles = mt * nt * splits, full = tiles / 256, rest = tiles % 256;
+    const double part = rest > 128 ? c.pair + (c.pair_all - c.pair) * (double)(rest - 128) / 128 : c.pair;
+    double t = c.fixed + (double)(full + (rest > 0) - 1) * c.round +
+               (double)((pairs_in(kbytes) + splits - 1) / splits) * ((double)full * c.pair_all + (rest ? part : 0));
+    t = std::max(t, c.fixed + (double)(rows + cols) * (double)kbytes / 4.9e6);
+    if (splits > 1) t += 3.5 + (double)rows * (double)cols * splits * 4 / 2.5e6;
+    return {shape, splits, (int)mt, (int)nt, t};
+}
+
 inline Plan plan_of(int64_t rows, int64_t cols, int64_t kbytes)
 {
-    struct Cost {
-        int tm, tn;
-        double fixed, round, pair, pair_all;
+    Plan best = plan_with(0, 1, rows, cols, kbytes);
+    auto offer = [&](const Plan &p) {
+        if (p.us < best.us) best = p;
     };
-    static constexpr Cost kCost[3] = {{256, 256, 6.0, 4.0, 1.03, 1.5}, {128, 128, 5.5, 3.0, 0.35, 0.485}, {64, 128, 4.5, 1.5, 0.28, 0.31}};
-    const int64_t pairs = kbytes > 128 ? (kbytes + 127) / 128 : 1;
-    Plan best{};
-    double least = 0;
+    for (int s = 1; s < 3; ++s) offer(plan_with(s, 1, rows, cols, kbytes));
+    // a split keeps at least four pairs, and splits never make more workgroups than two rounds
+    const int64_t mid = ((rows + 127) / 128) * ((cols + 127) / 128), pairs = pairs_in(kbytes);
+    for (int n = 2; n <= 8 && pairs >= 4 * n && mid * n <= 512; ++n) offer(plan_with(1, n, rows, cols, kbytes));
+    return best;
+}
+
+// Two products that do not depend on each other, x and w: with `together`
+// set both have one shape and no splits and go out as one launch, whose
+// workgroups fill the compute units that the last round of one of them alone
+// would leave idle.  Measured for the gradients of a gated block (us, two
+// launches / one): 1003 x 1408 x 2048 47.1 / 38.2, 256 x 512 x 1024 16.1 / 11.6,
+// 8192 x 1408 x 2048 225 / 207; 700 x 4096 x 1024, whose dX has few tiles and
+// long K, 51.3 (dX in parts) / 59.6.
+struct PlanPair {
+    Plan x, w;
+    bool together;
+};
+inline PlanPair plan_pair(int64_t xr, int64_t xc, int64_t xk, int64_t wr, int64_t wc, int64_t wk)
+{
+    PlanPair best{plan_of(xr, xc, xk), plan_of(wr, wc, wk), false};
+    double least = best.x.us + best.w.us;
     for (int s = 0; s < 3; ++s) {
-        const Cost &c = kCost[s];
-        const int64_t mt = (rows + c.tm - 1) / c.tm, nt = (cols + c.tn - 1) / c.tn;
-        // a split keeps at least four pairs, and splits never make more workgroups than two rounds
-        for (int n = 1; n == 1 || (s == 1 && n <= 8 && pairs >= 4 * n && mt * nt * n <= 512); ++n) {
-            const int64_t tiles = mt * nt * n, full = tiles / 256, rest = tiles % 256;
-            const double part = rest > 128 ? c.pair + (c.pair_all - c.pair) * (double)(rest - 128) / 128 : c.pair;
-            double t = c.fixed + (double)(full + (rest > 0) - 1) * c.round +
-                       (double)((pairs + n - 1) / n) * ((double)full * c.pair_all + (rest ? part : 0));
-            t = std::max(t, c.fixed + (double)(rows + cols) * (double)kbytes / 4.9e6);
-            if (n > 1) t += 3.5 + (double)rows * (double)cols * n * 4 / 2.5e6;
-            if (!best.splits || t < least) {
-                best = {s, n, (int)mt, (int)nt, t};
-                least = t;
-            }
+        const ShapeCost &c = kShapeCost[s];
+        const Plan x = plan_with(s, 1, xr, xc, xk), w = plan_with(s, 1, wr, wc, wk);
+        const double xt = (double)x.mt * x.nt, wt = (double)w.mt * w.nt, xp = (double)pairs_in(xk), wp = (double)pairs_in(wk);
+        // the longest tile among all the others (Small ones come to share
+        // a compute unit two by two), or the compute units kept busy to the end
+        const double share = s == 2 ? 1 + std::min(1.0, std::max(0.0, (xt + wt - 256) / 256)) : 1;
+        const double one = std::max(xp, wp) * (c.pair + c.pair_all) / 2 * share + c.fixed;
+        const double all = (xt * xp + wt * wp) / 256 * c.pair_all + c.fixed + c.round * ((xt + wt) / 256);
+        const double t = std::max(one, all);
+        if (t < least) {
+            best = {x, w, true};
+            least = t;
         }
     }
     return best;
