@@ -5,23 +5,15 @@ namespace bsg {
 namespace ffn {
 namespace {
 
+// Element i of a float tensor of a run-time type.  No branch on the type: the
+// loads of several elements then go out together (two halves of an fp32).
 __device__ __forceinline__ float load_float(const void *p, int64_t i, int dt)
 {
-    return dt == DT_F32 ? ((const float *)p)[i] : dt == DT_F16 ? (float)((const _Float16 *)p)[i] : (float)((const __bf16 *)p)[i];
-}
-
-// Scales four sums of row r from column c on, adds the bias and stores them.
-template <int CT>
-__device__ __forceinline__ void finish4(const I8Args &p, int64_t r, int64_t c, float4 s)
-{
-    const float rs = p.a_scale[r], *const cs = p.b_scale + c;
-    float b[4] = {0, 0, 0, 0};
-    if (p.bias) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) b[e] = load_float(p.bias, c + e, p.bias_dtype);
-    }
-    store4<CT>(p.c, r * p.n + c, make_float4(s.x * rs * cs[0] + b[0], s.y * rs * cs[1] + b[1], s.z * rs * cs[2] + b[2],
-                                             s.w * rs * cs[3] + b[3]));
+    const bool f32 = dt == DT_F32;
+    const uint16_t *const h = (const uint16_t *)p + (f32 ? 2 * i : i);
+    const uint32_t lo = h[0], hi = h[f32 ? 1 : 0];
+    const float half = (float)__builtin_bit_cast(_Float16, (uint16_t)lo), wide = __uint_as_float(hi << 16 | (f32 ? lo : 0u));
+    return dt == DT_F16 ? half : wide;
 }
 
 // ---------------------------------------------------------------------------
@@ -103,7 +95,20 @@ template <int CT>
 __global__ __launch_bounds__(256) void k_i8_join(I8Args p, int splits)
 {
     const int64_t i = 256ll * blockIdx.x + threadIdx.x, n4 = p.n / 4;
-    if (i < p.m * n4) finish4<CT>(p, i / n4, i % n4 * 4, join4<IN_I8>((const float *)p.workspace + 4 * i, p.m * p.n, splits));
+    if (i >= p.m * n4) return;
+    const int64_t r = i / n4, c = i % n4 * 4;
+    // (scales and bias on their way before the sums, which take longest)
+    const float rs = p.a_scale[r], *const cs = p.b_scale + c;
+    const float s0 = cs[0], s1 = cs[1], s2 = cs[2], s3 = cs[3];
+    float b0 = 0, b1 = 0, b2 = 0, b3 = 0;
+    if (p.bias) {
+        b0 = load_float(p.bias, c, p.bias_dtype);
+        b1 = load_float(p.bias, c + 1, p.bias_dtype);
+        b2 = load_float(p.bias, c + 2, p.bias_dtype);
+        b3 = load_float(p.bias, c + 3, p.bias_dtype);
+    }
+    const float4 s = join4<IN_I8>((const float *)p.workspace + 4 * i, p.m * p.n, splits);
+    store4<CT>(p.c, 4 * i, make_float4(s.x * rs * s0 + b0, s.y * rs * s1 + b1, s.z * rs * s2 + b2, s.w * rs * s3 + b3));
 }
 
 // ---------------------------------------------------------------------------
@@ -118,13 +123,25 @@ __global__ __launch_bounds__(kFewThreads) void k_i8_few(I8Args p)
     const uint8_t *const wrow = (const uint8_t *)p.b + min(c0 + (lane & 15), p.n - 1) * p.k, *xrow[MB];
 #pragma unroll
     for (int b = 0; b < MB; ++b) xrow[b] = (const uint8_t *)p.a + min((int64_t)16 * b + (lane & 15), p.m - 1) * p.k;
+    // this thread's outputs, (token, channel) number threadIdx.x + 512 e; their
+    // scales come while the weights do
+    constexpr int N = (16 * 16 * MB + kFewThreads - 1) / kFewThreads;
+    float rs[N], cs[N], bias[N];
+    const int ch = threadIdx.x % 16;
+    const int64_t c = c0 + ch;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        const int tk = (threadIdx.x + kFewThreads * e) / 16;
+        const bool in = tk < p.m && c < p.n;
+        rs[e] = in ? p.a_scale[tk] : 0.0f;
+        cs[e] = in ? p.b_scale[c] : 0.0f;
+        bias[e] = in && p.bias ? load_float(p.bias, c, p.bias_dtype) : 0.0f;
+    }
     few_sums<IN_I8, MB, U>(red, wrow, xrow, (int)p.k);
-    for (int i = threadIdx.x; i < 16 * (int)p.m; i += kFewThreads) {
-        const int ch = i % 16, tk = i / 16;
-        const int64_t c = c0 + ch;
-        if (c >= p.n) continue;
-        const float bias = p.bias ? load_float(p.bias, c, p.bias_dtype) : 0.0f;
-        store_one<CT>(p.c, tk * p.n + c, few_join<IN_I8, MB>(red, tk, ch) * p.a_scale[tk] * p.b_scale[c] + bias);
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        const int tk = (threadIdx.x + kFewThreads * e) / 16;
+        if (tk < p.m && c < p.n) store_one<CT>(p.c, tk * p.n + c, few_join<IN_I8, MB>(red, tk, ch) * rs[e] * cs[e] + bias[e]);
     }
 }
 

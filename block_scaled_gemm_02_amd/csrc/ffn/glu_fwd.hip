@@ -5,24 +5,6 @@ namespace bsg {
 namespace ffn {
 namespace {
 
-// Scales, gates and stores four columns of row r from column c on.
-template <int IN, int DT, int ACT, bool SAVE>
-__device__ __forceinline__ void finish4(const GluArgs &p, int64_t r, int64_t c, float4 g, float4 u)
-{
-    if constexpr (IN == IN_I8) {
-        const float rs = p.x_scale[r], *const gs = p.gate_scale + c, *const us = p.up_scale + c;
-        g = make_float4(g.x * rs * gs[0], g.y * rs * gs[1], g.z * rs * gs[2], g.w * rs * gs[3]);
-        u = make_float4(u.x * rs * us[0], u.y * rs * us[1], u.z * rs * us[2], u.w * rs * us[3]);
-    }
-    const int64_t o = r * p.n + c;
-    store4<DT>(p.h, o, make_float4(act_value<ACT>(g.x) * u.x, act_value<ACT>(g.y) * u.y, act_value<ACT>(g.z) * u.z,
-                                   act_value<ACT>(g.w) * u.w));
-    if constexpr (SAVE) {
-        store4<DT>(p.g, o, g);
-        store4<DT>(p.u, o, u);
-    }
-}
-
 // A tile holds TN / 2 columns of H: of the B panel's rows for each wave's
 // quadrant half are gate rows and half the up rows of the same columns, so
 // that a lane's gate and up sums belong to the same elements of H.  DT: the type of H (and of G and U, stored if SAVE).
@@ -128,8 +110,26 @@ __global__ __launch_bounds__(256) void k_glu_join(GluArgs p, int splits)
     if (i >= p.m * n4) return;
     const int64_t r = i / n4, c = i % n4 * 4;
     const float *const src = (const float *)p.workspace + r * 2 * p.n + c;
-    finish4<IN, DT, ACT, SAVE>(p, r, c, join4<IN>(src, 2 * p.m * p.n, splits),
-                               join4<IN>(src + p.n, 2 * p.m * p.n, splits));
+    float gs[4], us[4], rs = 0;
+    if constexpr (IN == IN_I8) {
+        rs = p.x_scale[r];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            gs[e] = p.gate_scale[c + e];
+            us[e] = p.up_scale[c + e];
+        }
+    }
+    float4 g = join4<IN>(src, 2 * p.m * p.n, splits), u = join4<IN>(src + p.n, 2 * p.m * p.n, splits);
+    if constexpr (IN == IN_I8) {
+        g = make_float4(g.x * rs * gs[0], g.y * rs * gs[1], g.z * rs * gs[2], g.w * rs * gs[3]);
+        u = make_float4(u.x * rs * us[0], u.y * rs * us[1], u.z * rs * us[2], u.w * rs * us[3]);
+    }
+    store4<DT>(p.h, 4 * i, make_float4(act_value<ACT>(g.x) * u.x, act_value<ACT>(g.y) * u.y, act_value<ACT>(g.z) * u.z,
+                                       act_value<ACT>(g.w) * u.w));
+    if constexpr (SAVE) {
+        store4<DT>(p.g, 4 * i, g);
+        store4<DT>(p.u, 4 * i, u);
+    }
 }
 
 // A few tokens: of a workgroup's 16 weight rows 8 are gate rows and 8 the up
@@ -143,20 +143,28 @@ __global__ __launch_bounds__(kFewThreads) void k_glu_few(GluArgs p)
     const uint8_t *const wrow = (const uint8_t *)(lane & 8 ? p.w_up : p.w_gate) + (c0 + (lane & 7)) * ld, *xrow[MB];
 #pragma unroll
     for (int b = 0; b < MB; ++b) xrow[b] = (const uint8_t *)p.x + min((int64_t)16 * b + (lane & 15), p.m - 1) * ld;
+    // this thread's output; its scales come while the weights do
+    static_assert(8 * 16 * MB <= kFewThreads, "one output a thread");
+    const int ch = threadIdx.x % 8, tk = threadIdx.x / 8;
+    const int64_t c = c0 + ch, o = tk * p.n + c;
+    const bool in = tk < p.m;
+    float rs = 0, gs = 0, us = 0;
+    if (IN == IN_I8 && in) {
+        rs = p.x_scale[tk];
+        gs = p.gate_scale[c];
+        us = p.up_scale[c];
+    }
     few_sums<IN, MB, U>(red, wrow, xrow, (int)ld);
-    for (int i = threadIdx.x; i < 8 * (int)p.m; i += kFewThreads) {
-        const int ch = i % 8, tk = i / 8;
-        const int64_t c = c0 + ch, o = tk * p.n + c;
-        float g = few_join<IN, MB>(red, tk, ch), u = few_join<IN, MB>(red, tk, 8 + ch);
-        if constexpr (IN == IN_I8) {
-            g = g * p.x_scale[tk] * p.gate_scale[c];
-            u = u * p.x_scale[tk] * p.up_scale[c];
-        }
-        store_one<DT>(p.h, o, act_value<ACT>(g) * u);
-        if constexpr (SAVE) {
-            store_one<DT>(p.g, o, g);
-            store_one<DT>(p.u, o, u);
-        }
+    if (!in) return;
+    float g = few_join<IN, MB>(red, tk, ch), u = few_join<IN, MB>(red, tk, 8 + ch);
+    if constexpr (IN == IN_I8) {
+        g = g * rs * gs;
+        u = u * rs * us;
+    }
+    store_one<DT>(p.h, o, act_value<ACT>(g) * u);
+    if constexpr (SAVE) {
+        store_one<DT>(p.g, o, g);
+        store_one<DT>(p.u, o, u);
     }
 }
 
