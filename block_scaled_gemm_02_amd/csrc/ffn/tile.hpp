@@ -8,12 +8,12 @@
 // row r.  K advances in pairs of 128 bytes a row (one whole line), in two
 // steps of 64 bytes (two MFMAs a block).
 //
-// The LDS holds a ring of NS pair slots, filled by direct-to-LDS loads
-// (buffer_load_dwordx4 ... lds) that no register passes through; reads past a
-// row, a tensor or the K range return zeros (buffer range check), which is
-// all that ragged sizes need.  Within a pair's second step the slot of the
-// pair is free (its last fragments are in registers, and a barrier says so
-// for all waves), and the loads of the pair NS further on go out between the
+// The LDS holds a ring of panels, a pair of A or B each, filled by
+// direct-to-LDS loads (buffer_load_dwordx4 ... lds) that no register passes
+// through; reads past a row, a tensor or the K range return zeros (buffer
+// range check), which is all that ragged sizes need.  Within a pair's second
+// step its slots are free (its last fragments are in registers, and a barrier
+// says so for all waves), and the loads of a later pair go out between the
 // MFMAs.  The fragments of the next step are read between the MFMAs too.
 //
 // k-major panel (rows of K): row r at 128 r, its 16-byte chunk c at position
@@ -69,7 +69,7 @@ struct Loader {
     const uint8_t *base;
     int64_t bytes, step;
     i32x4 r;
-    uint32_t v[L], pv, klimit, chunk[2], add[2], padd;
+    uint32_t v[L], klimit, chunk[2], add[2];
 
     __device__ __forceinline__ void init_k(const uint8_t *b, int64_t n, int64_t ld, int64_t kbytes, int w, int lane)
     {
@@ -82,7 +82,6 @@ struct Loader {
         chunk[1] = chunk[0] ^ 16;
 #pragma unroll
         for (int q = 0; q < L; ++q) v[q] = (8 * q + row) * (uint32_t)ld + chunk[q & 1];
-        pv = lane < T / 4 ? (uint32_t)lane * (uint32_t)ld : kOOB;
     }
     __device__ __forceinline__ void init_mn(const uint8_t *b, int64_t n, int64_t ld, int64_t cols, int w, int lane)
     {
@@ -96,9 +95,6 @@ struct Loader {
             const uint32_t col = o ^ (64u * mn_swizzle<T>(kk));
             v[q] = col < valid ? kk * (uint32_t)ld + col : kOOB;
         }
-        constexpr uint32_t LPR = T / 64;       // lines of a K row
-        const uint32_t line = 128u * ((uint32_t)lane % LPR);
-        pv = (uint32_t)lane < 16 * LPR && line < valid ? (16u * w + (uint32_t)lane / LPR) * (uint32_t)ld + line : kOOB;
     }
     // Aims the loads at a pair.
     __device__ __forceinline__ void seek(int pair)
@@ -107,11 +103,9 @@ struct Loader {
             const uint32_t kb = (uint32_t)pair * 128u;
             add[0] = kb + chunk[0] < klimit ? kb : kOOB;
             add[1] = kb + chunk[1] < klimit ? kb : kOOB;
-            padd = kb < klimit ? kb : kOOB;
         } else {
             const int64_t off = (int64_t)pair * step;
             r = make_rsrc_words(base + off, clamp_bytes(bytes - off));
-            padd = 0;
         }
     }
     template <int Q>
@@ -119,8 +113,6 @@ struct Loader {
     {
         lds_load16(r, panel + 1024 * (L * w + Q), v[Q] + (KM ? add[Q & 1] : 0u));
     }
-    // Touches the lines of the pair, so that its loads find them in the L2.
-    __device__ __forceinline__ void prefetch(uint8_t *sink, int w) const { lds_load4(r, sink + 256 * w, pv + padd); }
 };
 
 // Fragment reads of one wave from a panel: C chunks of 32 rows each.
@@ -170,15 +162,19 @@ struct Frag {
     i32x4 a[MI][2], b[NB][2];
 };
 
-// The ring of a tile and the K loop over it.
-template <int IN, bool AK, bool BK, int MI, int NB, int NS, bool PF>
+// The ring of a tile and the K loop over it: NA slots for A panels, NB_ for
+// B panels.  With one more for B (NB_ = NA + 1 = 3, the largest tile, whose
+// ring then fills the 160 KB) the loads of a pair are staggered: B's go out a
+// step before A's, half as many a step, and have a step longer to land.
+template <int IN, bool AK, bool BK, int MI, int NB, int NA, int NB_>
 struct Tile {
     static constexpr int TM = 64 * MI, TN = 64 * NB;
-    static constexpr int kA = TM * 128, kSlot = kA + TN * 128, kRing = NS * kSlot, kLds = kRing + (PF ? 1024 : 0);
+    static constexpr bool STAG = NB_ > NA;
+    static_assert(NB_ == NA || (STAG && NA == 2 && NB_ == 3), "the ring's slots");
+    static constexpr int kA = TM * 128, kB = TN * 128, kRing = NA * kA + NB_ * kB, kLds = kRing;
     static constexpr int kStage = kRing / 4 & ~15;          // epilogue staging bytes of a wave
     typedef Loader<AK, TM> LA;
     typedef Loader<BK, TN> LB;
-    static constexpr int LP = LA::L + LB::L;                // loads of a pair and wave
     static constexpr int kM = 2 * MI * NB;                  // MFMAs of a step
     Reader<AK, TM, MI> ra;
     Reader<BK, TN, NB> rb;
@@ -186,33 +182,37 @@ struct Tile {
     static constexpr int kRSpan = kM * 3 / 4 > 0 ? kM * 3 / 4 : 1;
 
     template <int H, int Q>
-    __device__ __forceinline__ void read1(Frag<MI, NB> &f, const uint8_t *slot) const
+    __device__ __forceinline__ void read1(Frag<MI, NB> &f, const uint8_t *pa, const uint8_t *pb) const
     {
         constexpr int RA = Reader<AK, TM, MI>::kReads;
-        if constexpr (Q < RA) ra.template read<H, Q>(f.a, slot);
-        else rb.template read<H, Q - RA>(f.b, slot + kA);
+        if constexpr (Q < RA) ra.template read<H, Q>(f.a, pa);
+        else rb.template read<H, Q - RA>(f.b, pb);
     }
-    template <int Q>
-    __device__ __forceinline__ void load1(const LA &la, const LB &lb, uint8_t *slot, int w) const
+    // Load Q of a step that loads A (WA) and / or B panels.
+    template <bool WA, int Q>
+    __device__ __forceinline__ void load1(const LA &la, const LB &lb, uint8_t *pa, uint8_t *pb, int w) const
     {
-        if constexpr (Q < LA::L) la.template load<Q>(slot, w);
-        else lb.template load<Q - LA::L>(slot + kA, w);
+        if constexpr (WA && Q < LA::L) la.template load<Q>(pa, w);
+        else lb.template load<Q - (WA ? LA::L : 0)>(pb, w);
     }
 
-    // One step: MFMAs on cur, fragments of the next step (half NH of rslot)
-    // into nxt, and, in a pair's second step, the loads of a later pair.
+    // One step: MFMAs on cur, fragments of the next step (of panels ra_, rb_)
+    // into nxt, and loads into the panels pa and pb.
     template <bool ODD, class Seek>
     __device__ __forceinline__ void step(f32x16 (&acc)[MI][NB], Frag<MI, NB> &cur, Frag<MI, NB> &nxt, LA &la, LB &lb,
-                                         const uint8_t *rslot, uint8_t *lslot, uint8_t *sink, int w, Seek &&seek)
+                                         const uint8_t *ra_, const uint8_t *rb_, uint8_t *pa, uint8_t *pb, int w, Seek &&seek)
     {
+        constexpr bool WA = ODD, WB = ODD != STAG;
+        constexpr int L = (WA ? LA::L : 0) + (WB ? LB::L : 0);
         if constexpr (ODD) {
-            // the next pair has landed: what may be in flight is the pairs after it and one prefetch
-            s_wait_vm<(NS - 2) * LP + (PF ? 1 : 0)>();
+            // the next pair has landed; what may be in flight are the pairs
+            // after it, or (staggered) the B panel after it
+            s_wait_vm<STAG ? LB::L : (NA - 2) * (LA::L + LB::L)>();
             s_wait_lgkm0();
             __builtin_amdgcn_s_barrier();
         } else {
             s_wait_lgkm0();
-            seek();                  // aim at the pair that the next step loads
+            seek();                  // aim at the pair that this step and the next one load
         }
         __builtin_amdgcn_sched_barrier(0);
         static_for<kM>([&](auto mm) {
@@ -220,16 +220,12 @@ struct Tile {
             acc[i][j] = mfma32<IN>(cur.b[j][S], cur.a[i][S], acc[i][j]);
             if constexpr (m < kRSpan) {
                 static_for<(kR * (m + 1)) / kRSpan - (kR * m) / kRSpan>([&](auto rr) {
-                    read1<ODD ? 0 : 1, (kR * m) / kRSpan + decltype(rr)::value>(nxt, rslot);
+                    read1<ODD ? 0 : 1, (kR * m) / kRSpan + decltype(rr)::value>(nxt, ra_, rb_);
                 });
             }
-            if constexpr (ODD) {
-                static_for<(LP * (m + 1)) / kM - (LP * m) / kM>([&](auto ll) {
-                    load1<(LP * m) / kM + decltype(ll)::value>(la, lb, lslot, w);
-                });
-            } else if constexpr (PF && m == 0) {
-                la.prefetch(sink, w);
-            }
+            static_for<(L * (m + 1)) / kM - (L * m) / kM>([&](auto ll) {
+                load1<WA, (L * m) / kM + decltype(ll)::value>(la, lb, pa, pb, w);
+            });
             __builtin_amdgcn_sched_barrier(0);
         });
     }
@@ -249,24 +245,28 @@ struct Tile {
                 for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
         ra.init(32 * MI * (w >> 1), lane);
         rb.init(32 * NB * (w & 1), lane);
-        uint8_t *const sink = ring + kRing;
+        uint8_t *const ringb = ring + NA * kA;
 #pragma unroll
-        for (int s = 0; s < NS; ++s) {
+        for (int s = 0; s < NA; ++s) {
             seek(s);
-            static_for<LP>([&](auto q) { load1<decltype(q)::value>(la, lb, ring + s * kSlot, w); });
+            static_for<LA::L + LB::L>([&](auto q) { load1<true, decltype(q)::value>(la, lb, ring + s * kA, ringb + s * kB, w); });
         }
-        s_wait_vm<(NS - 1) * LP>();
+        s_wait_vm<(NA - 1) * (LA::L + LB::L)>();
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
         Frag<MI, NB> fx, fy;
-        static_for<kR>([&](auto q) { read1<0, decltype(q)::value>(fx, ring); });
-        uint8_t *slot = ring;
+        static_for<kR>([&](auto q) { read1<0, decltype(q)::value>(fx, ring, ringb); });
+        auto next_a = [&](uint8_t *p) { return p == ring + (NA - 1) * kA ? ring : p + kA; };
+        auto next_b = [&](uint8_t *p) { return p == ringb + (NB_ - 1) * kB ? ringb : p + kB; };
+        uint8_t *a = ring, *b = ringb;                      // panels of the current pair
         int pair = 0;
         do {
-            uint8_t *const next = slot == ring + (NS - 1) * kSlot ? ring : slot + kSlot;
-            step<false>(acc, fx, fy, la, lb, slot, slot, sink, w, [&] { seek(pair + NS); });
-            step<true>(acc, fy, fx, la, lb, next, slot, sink, w, [] {});
-            slot = next;
+            uint8_t *const a1 = next_a(a), *const b1 = next_b(b);
+            // staggered: the B panel two pairs on has a slot of its own already
+            step<false>(acc, fx, fy, la, lb, a, b, a, STAG ? next_b(b1) : b, w, [&] { seek(pair + NA); });
+            step<true>(acc, fy, fx, la, lb, a1, b1, a, b, w, [] {});
+            a = a1;
+            b = b1;
         } while (++pair < np);
         s_wait_vm<0>();
         s_wait_lgkm0();
@@ -305,16 +305,16 @@ __device__ __forceinline__ void store4(void *p, int64_t i, float4 v)
 // cycles of MFMA.  (Letting the four waves divide a pair's K instead of the
 // tile, so that no fragment is read from LDS twice, gained nothing for that
 // reason and its joining of the four sums cost 2 us.)
-template <int MI_, int NB_, int NS_, bool PF_>
+template <int MI_, int NB_, int SA, int SB>
 struct Shape {
     static constexpr int MI = MI_, NB = NB_, TM = 64 * MI, TN = 64 * NB;
     static constexpr int kWaves = MI * NB == 16 ? 1 : 2;     // waves a SIMD that the registers allow
     template <int IN, bool AK, bool BK>
-    using Of = Tile<IN, AK, BK, MI, NB, NS_, PF_>;
+    using Of = Tile<IN, AK, BK, MI, NB, SA, SB>;
 };
-typedef Shape<4, 4, 2, true> Big;
-typedef Shape<2, 2, 4, false> Mid;
-typedef Shape<1, 2, 3, false> Small;
+typedef Shape<4, 4, 2, 3> Big;
+typedef Shape<2, 2, 4, 4> Mid;
+typedef Shape<1, 2, 3, 3> Small;
 
 // K divided over workgroups, where a product has fewer tiles than the card
 // has compute units: split s of `splits` sums the pairs [first, first + count)
