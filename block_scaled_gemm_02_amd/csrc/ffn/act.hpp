@@ -8,7 +8,6 @@ namespace bsg {
 namespace ffn {
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef int i32x16 __attribute__((ext_vector_type(16)));
 
 // sigmoid(t) and 1 - sigmoid(t) from one exponential of -|t|, which never
 // overflows: with e = exp(-|t|) and r = 1 / (1 + e), the two are r and e*r.

@@ -40,17 +40,17 @@ __global__ __launch_bounds__(256, S::kWaves) void k_i8(I8Args p, int mt, int nt,
         la.seek(sp.at(pair));
         lb.seek(sp.at(pair));
     };
-    f32x16 acc[MI][NB];
+    f32x4 acc[2 * MI][2 * NB];
     T t;
     const int64_t r0 = m0 + 32 * MI * (w >> 1), c0 = n0 + 32 * NB * (w & 1);
     const int rows = (int)min((int64_t)32 * MI, p.m - r0), cols = (int)min((int64_t)32 * NB, p.n - c0);
-    // scales and bias, in registers over the K loop: a row's for each block,
+    // scales and bias, in registers over the K loop: a row's for each 16-row block,
     // and columns l and l + 64 of the wave's in lane l
     constexpr int CL = (NB + 1) / 2;
-    float rs[MI], sc[CL], bi[CL];
+    float rs[2 * MI], sc[CL], bi[CL];
     if constexpr (!SPLIT) {
 #pragma unroll
-        for (int i = 0; i < MI; ++i) rs[i] = 32 * i + (lane & 31) < rows ? p.a_scale[r0 + 32 * i + (lane & 31)] : 0.0f;
+        for (int i = 0; i < 2 * MI; ++i) rs[i] = 16 * i + (lane & 15) < rows ? p.a_scale[r0 + 16 * i + (lane & 15)] : 0.0f;
 #pragma unroll
         for (int h = 0; h < CL; ++h) {
             const int c = lane + 64 * h;
@@ -74,15 +74,14 @@ __global__ __launch_bounds__(256, S::kWaves) void k_i8(I8Args p, int mt, int nt,
         static_for<MI>([&](auto ii) {
             constexpr int i = decltype(ii)::value;
             __builtin_amdgcn_sched_barrier(0);
-            pin(acc[i]);
-            stage_block<CT, NB>(reg, lane, [&](auto jj, auto qq) {
-                constexpr int j = decltype(jj)::value, q = decltype(qq)::value;
-                const int c = 32 * j + 8 * q + 4 * (lane >> 5);
+            pin(acc[2 * i], acc[2 * i + 1]);
+            stage_block<CT, NB>(reg, lane, [&](auto hh, auto jj) {
+                constexpr int r = 2 * i + decltype(hh)::value, j = decltype(jj)::value;
+                const int c = 16 * j + 4 * (lane >> 4);
                 const float4 s = *reinterpret_cast<const float4 *>(cs + c), b = *reinterpret_cast<const float4 *>(cb + c);
-                return make_float4((float)__float_as_int(acc[i][j][4 * q]) * rs[i] * s.x + b.x,
-                                   (float)__float_as_int(acc[i][j][4 * q + 1]) * rs[i] * s.y + b.y,
-                                   (float)__float_as_int(acc[i][j][4 * q + 2]) * rs[i] * s.z + b.z,
-                                   (float)__float_as_int(acc[i][j][4 * q + 3]) * rs[i] * s.w + b.w);
+                const f32x4 x = acc[r][j];
+                return make_float4((float)__float_as_int(x[0]) * rs[r] * s.x + b.x, (float)__float_as_int(x[1]) * rs[r] * s.y + b.y,
+                                   (float)__float_as_int(x[2]) * rs[r] * s.z + b.z, (float)__float_as_int(x[3]) * rs[r] * s.w + b.w);
             });
             flush_block<ES, NB>(reg, (char *)p.c + ES * ((r0 + 32 * i) * p.n + c0), (uint32_t)(ES * p.n), rows - 32 * i,
                                 ES * cols, lane);

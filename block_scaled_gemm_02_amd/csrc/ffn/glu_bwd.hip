@@ -35,16 +35,16 @@ __global__ __launch_bounds__(256) void k_dact(const uint4 *dh, const uint4 *g, c
     d[r * 2 * n8 + n8 + c] = b;
 }
 
-template <int DT, int MI, int NB, class Flush>
-__device__ __forceinline__ void store16(f32x16 (&acc)[MI][NB], uint8_t *reg, int lane, Flush &&flush)
+template <int DT, int M2, int N2, class Flush>
+__device__ __forceinline__ void store16(f32x4 (&acc)[M2][N2], uint8_t *reg, int lane, Flush &&flush)
 {
-    static_for<MI>([&](auto ii) {
+    static_for<M2 / 2>([&](auto ii) {
         constexpr int i = decltype(ii)::value;
         __builtin_amdgcn_sched_barrier(0);
-        pin(acc[i]);
-        stage_block<DT, NB>(reg, lane, [&](auto jj, auto qq) {
-            constexpr int j = decltype(jj)::value, q = decltype(qq)::value;
-            return make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+        pin(acc[2 * i], acc[2 * i + 1]);
+        stage_block<DT, N2 / 2>(reg, lane, [&](auto hh, auto jj) {
+            const f32x4 x = acc[2 * i + decltype(hh)::value][decltype(jj)::value];
+            return make_float4(x[0], x[1], x[2], x[3]);
         });
         flush(i);
     });
@@ -79,7 +79,7 @@ __device__ __forceinline__ void dx_tile(const GluBwdArgs &p, const uint8_t *d, f
         la.seek(up ? q - np : q);
         lb.seek(up ? q - np : q);
     };
-    f32x16 acc[MI][NB];
+    f32x4 acc[2 * MI][2 * NB];
     T t;
     t.run(acc, ring, la, lb, sp.count, seek);
     const int64_t r0 = m0 + 32 * MI * (w >> 1), c0 = n0 + 32 * NB * (w & 1);
@@ -114,7 +114,7 @@ __device__ __forceinline__ void dw_tile(const GluBwdArgs &p, const uint8_t *d, f
         la.seek(sp.at(pair));
         lb.seek(sp.at(pair));
     };
-    f32x16 acc[MI][NB];
+    f32x4 acc[2 * MI][2 * NB];
     T t;
     t.run(acc, ring, la, lb, sp.count, seek);
     const int64_t r0 = m0 + 32 * MI * (w >> 1), c0 = n0 + 32 * NB * (w & 1);

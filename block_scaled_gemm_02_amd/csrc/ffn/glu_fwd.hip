@@ -30,17 +30,17 @@ __global__ __launch_bounds__(256, S::kWaves) void k_glu(GluArgs p, int mt, int n
         la.seek(sp.at(pair));
         lb.seek(sp.at(pair));
     };
-    f32x16 acc[MI][NB];
+    f32x4 acc[2 * MI][2 * NB];
     T t;
     constexpr int HW = NB / 2, HC = 32 * HW;
     const int64_t r0 = m0 + 32 * MI * (w >> 1), c0 = h0 + HC * (w & 1);
     const int rows = (int)min((int64_t)32 * MI, p.m - r0), cols = (int)min((int64_t)HC, p.n - c0);
-    // scales, in registers over the K loop: a row's for each block, and of the
+    // scales, in registers over the K loop: a row's for each 16-row block, and of the
     // wave's HC <= 64 columns lane l holds gate (l) and up scale
-    float rs[MI], gs = 0.0f, us = 0.0f;
+    float rs[2 * MI], gs = 0.0f, us = 0.0f;
     if constexpr (IN == IN_I8 && !SPLIT) {
 #pragma unroll
-        for (int i = 0; i < MI; ++i) rs[i] = 32 * i + (lane & 31) < rows ? p.x_scale[r0 + 32 * i + (lane & 31)] : 0.0f;
+        for (int i = 0; i < 2 * MI; ++i) rs[i] = 16 * i + (lane & 15) < rows ? p.x_scale[r0 + 16 * i + (lane & 15)] : 0.0f;
         if (lane < cols) {
             gs = p.gate_scale[c0 + lane];
             us = p.up_scale[c0 + lane];
@@ -67,27 +67,28 @@ __global__ __launch_bounds__(256, S::kWaves) void k_glu(GluArgs p, int mt, int n
         static_for<MI>([&](auto ii) {
             constexpr int i = decltype(ii)::value;
             __builtin_amdgcn_sched_barrier(0);
-            pin(acc[i]);
-            // four gate (block column b) or up (b + HW) values of the lane's row
-            auto quad = [&](auto blk, auto qq) {
-                constexpr int b = decltype(blk)::value, q = decltype(qq)::value;
-                float4 x = make_float4(acc[i][b][4 * q], acc[i][b][4 * q + 1], acc[i][b][4 * q + 2], acc[i][b][4 * q + 3]);
-                if constexpr (IN == IN_I8) {
-                    const float4 s = *reinterpret_cast<const float4 *>(cs + 32 * b + 8 * q + 4 * (lane >> 5));
-                    x.x = (float)__float_as_int(x.x) * rs[i] * s.x;
-                    x.y = (float)__float_as_int(x.y) * rs[i] * s.y;
-                    x.z = (float)__float_as_int(x.z) * rs[i] * s.z;
-                    x.w = (float)__float_as_int(x.w) * rs[i] * s.w;
-                }
-                return x;
-            };
-            auto up = [&](auto j, auto q) { return quad(std::integral_constant<int, decltype(j)::value + HW>{}, q); };
-            auto h = [&](auto j, auto q) {
-                const float4 g = quad(j, q), u = up(j, q);
-                return make_float4(act_value<ACT>(g.x) * u.x, act_value<ACT>(g.y) * u.y, act_value<ACT>(g.z) * u.z,
-                                   act_value<ACT>(g.w) * u.w);
-            };
-            const int64_t o = 2 * ((r0 + 32 * i) * p.n + c0);
+            pin(acc[2 * i], acc[2 * i + 1]);
+        // four gate or up values (block column j) of row 16 hh + l%16
+        auto quad = [&](auto hh, auto jj) {
+            constexpr int r = 2 * i + decltype(hh)::value, j = decltype(jj)::value;
+            const f32x4 v = acc[r][j];
+            float4 x = make_float4(v[0], v[1], v[2], v[3]);
+            if constexpr (IN == IN_I8) {
+                const float4 s = *reinterpret_cast<const float4 *>(cs + 16 * j + 4 * (lane >> 4));
+                x.x = (float)__float_as_int(x.x) * rs[r] * s.x;
+                x.y = (float)__float_as_int(x.y) * rs[r] * s.y;
+                x.z = (float)__float_as_int(x.z) * rs[r] * s.z;
+                x.w = (float)__float_as_int(x.w) * rs[r] * s.w;
+            }
+            return x;
+        };
+        auto up = [&](auto hh, auto jj) { return quad(hh, std::integral_constant<int, decltype(jj)::value + 2 * HW>{}); };
+        auto h = [&](auto hh, auto jj) {
+            const float4 g = quad(hh, jj), u = up(hh, jj);
+            return make_float4(act_value<ACT>(g.x) * u.x, act_value<ACT>(g.y) * u.y, act_value<ACT>(g.z) * u.z,
+                               act_value<ACT>(g.w) * u.w);
+        };
+        const int64_t o = 2 * ((r0 + 32 * i) * p.n + c0);
             stage_block<DT, HW>(reg, lane, h);
             if constexpr (SAVE) {
                 stage_block<DT, HW>(reg + kReg, lane, quad);

@@ -1,12 +1,17 @@
 // The matrix-product tile of the feed-forward operators: a workgroup of four
 // wave64s computes a (64 MI) x (64 NB) tile, each wave a (32 MI) x (32 NB)
-// quadrant in 32x32 MFMA blocks whose accumulators stay in registers.
+// quadrant in 16x16 MFMA blocks whose accumulators stay in registers.
 //
 // Operands are bf16, fp16 or int8, and any of them is read in 16-byte chunks:
-// one MFMA of 32x32x16 (16 bits) or 32x32x32 (8 bits) takes one chunk a lane
-// and operand, lane (r = l%32, g = l/32) holding K bytes [16g, 16g + 16) of
+// one MFMA of 16x16x32 (16 bits) or 16x16x64 (8 bits) takes one chunk a lane
+// and operand, lane (r = l%16, g = l/16) holding K bytes [16g, 16g + 16) of
 // row r.  K advances in pairs of 128 bytes a row (one whole line), in two
-// steps of 64 bytes (two MFMAs a block).
+// steps of 64 bytes (one MFMA a block).  The 32x32 MFMAs need half the operand
+// reads and keep the matrix cores as busy, but their accumulators are read
+// and written twice as often, and at these sizes the card runs at its power
+// limit: on random operands the 16x16 ones are 9% faster (int8 8192^3 418 ->
+// 381 us) and 6% (bf16, gated 8192 x 8192 x 4096, 814 -> 763 us), though on
+// zeros they are 1% slower.
 //
 // The LDS holds a ring of panels, a pair of A or B each, filled by
 // direct-to-LDS loads (buffer_load_dwordx4 ... lds) that no register passes
@@ -20,10 +25,12 @@
 // c ^ s(r), s(r) = (r%8) ^ ((r/8)%2), so that the 16 lanes that a 128-bit
 // read serves at once cover all 64 banks.
 // mn-major panel (16-bit; rows of M or N at each K): K row kk at (2 T) kk, its
-// 64-byte block b at b ^ x(kk); the transposing read (ds_read_b64_tr_b16) of a
-// half wave takes 64 bytes from each of 4 consecutive K rows, which x puts on
-// different banks: kk%4, or (kk%4)/2 where a row has two blocks only (T = 64)
-// and its neighbour the other half of the banks.
+// 32-byte block b at b ^ x(kk).  The transposing read (ds_read_b64_tr_b16)
+// takes 32 bytes from each of 4 consecutive K rows in a 16-lane group, and
+// from the 4 rows 8 further on in the next group; x puts a half wave's 8
+// pieces on different banks: kk%4 in 64-byte steps ((kk%4)/2 where a row is
+// 128 bytes, T = 64, and its neighbour the other half of the banks) and
+// (kk/8)%2 in 32-byte ones.
 #pragma once
 #include "act.hpp"
 #include "plan.hpp"
@@ -31,21 +38,21 @@
 namespace bsg {
 namespace ffn {
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
 enum In : int { IN_BF16 = 0, IN_F16 = 1, IN_I8 = 2 };
 constexpr int in_bytes(int in) { return in == IN_I8 ? 1 : 2; }
 constexpr int dt_of(int in) { return in == IN_F16 ? DT_F16 : DT_BF16; }
 
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// acc += b a.  Written as assembly with the accumulator tied to AGPRs: of the
+// builtin's 64 four-register accumulators the compiler kept copying some
+// between the register files, 220 moves a pair of K.
 template <int IN>
-__device__ __forceinline__ f32x16 mfma32(const i32x4 &b, const i32x4 &a, const f32x16 &acc)
+__device__ __forceinline__ void mfma_into(f32x4 &acc, const i32x4 &b, const i32x4 &a)
 {
-    if constexpr (IN == IN_BF16)
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a), acc, 0, 0, 0);
-    else if constexpr (IN == IN_F16)
-        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, b), __builtin_bit_cast(f16x8, a), acc, 0, 0, 0);
-    else
-        return __builtin_bit_cast(f32x16, __builtin_amdgcn_mfma_i32_32x32x32_i8(b, a, __builtin_bit_cast(i32x16, acc), 0, 0, 0));
+    if constexpr (IN == IN_BF16) asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
+    else if constexpr (IN == IN_F16) asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
+    else asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
 }
 
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)); }
@@ -57,7 +64,10 @@ __device__ __forceinline__ int pairs_of(int64_t kbytes) { return kbytes > 128 ? 
 __device__ __forceinline__ uint32_t clamp_bytes(int64_t b) { return b <= 0 ? 0u : (b < 0x7FFFFFFF ? (uint32_t)b : 0x7FFFFFFFu); }
 
 template <int T>
-__device__ __forceinline__ uint32_t mn_swizzle(uint32_t kk) { return T == 64 ? (kk >> 1) & 1 : kk & 3; }
+__device__ __forceinline__ uint32_t mn_swizzle(uint32_t kk)
+{
+    return (kk >> 3 & 1) + 2 * (T == 64 ? kk >> 1 & 1 : kk & 3);
+}
 
 // One wave's share of the loads of a T-row panel: T/32 loads of 1 KB a pair.
 // k-major: rows T/4 w ...  of the panel, base at the first of them, `bytes`
@@ -92,7 +102,7 @@ struct Loader {
 #pragma unroll
         for (int q = 0; q < L; ++q) {
             const uint32_t p = 1024u * (L * w + q) + 16u * (uint32_t)lane, kk = p / (2 * T), o = p % (2 * T);
-            const uint32_t col = o ^ (64u * mn_swizzle<T>(kk));
+            const uint32_t col = o ^ (32u * mn_swizzle<T>(kk));
             v[q] = col < valid ? kk * (uint32_t)ld + col : kOOB;
         }
     }
@@ -108,50 +118,67 @@ struct Loader {
             r = make_rsrc_words(base + off, clamp_bytes(bytes - off));
         }
     }
+    // Load Q of the wave's share of the panel, in two parts that may stand
+    // apart (nothing else writes M0): its LDS address, and the load itself.
+    template <int Q>
+    __device__ __forceinline__ uint32_t prepare(uint8_t *panel, int w) const
+    {
+        const uint32_t m0 = (uint32_t)(uintptr_t)(lds_void *)(panel + 1024 * (L * w + Q));
+        asm volatile("s_mov_b32 m0, %0" : : "s"(m0));
+        return v[Q] + (KM ? add[Q & 1] : 0u);
+    }
+    __device__ __forceinline__ void issue(uint32_t voff) const
+    {
+        asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(voff), "s"(r) : "memory");
+    }
     template <int Q>
     __device__ __forceinline__ void load(uint8_t *panel, int w) const
     {
-        lds_load16(r, panel + 1024 * (L * w + Q), v[Q] + (KM ? add[Q & 1] : 0u));
+        const uint32_t voff = prepare<Q>(panel, w);
+        asm volatile("s_nop 0");            // one wait state between M0 and the load that reads it
+        issue(voff);
     }
 };
 
-// Fragment reads of one wave from a panel: C chunks of 32 rows each.
+// Fragment reads of one wave from a panel: C blocks of 16 rows.
 template <bool KM, int T, int C>
 struct Reader {
-    static constexpr int kReads = KM ? 2 * C : 4 * C;      // of a step
-    uint32_t off[KM ? 4 : C];
+    static constexpr int kReads = KM ? C : 2 * C;      // of a step
+    uint32_t off[KM ? 2 : C];
     // row0: the wave's first row (column) in the panel
     __device__ __forceinline__ void init(int row0, int lane)
     {
+        const uint32_t r = (uint32_t)lane & 15, g = (uint32_t)lane >> 4;
         if constexpr (KM) {
-            const uint32_t r = (uint32_t)lane & 31, g = (uint32_t)lane >> 5, s = (r & 7) ^ ((r >> 3) & 1);
+            // 16 rows on, s(r) exchanges the same positions
+            const uint32_t s = (r & 7) ^ (r >> 3);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) off[c] = ((uint32_t)row0 + r) * 128u + 16u * ((2u * c + g) ^ s);
+            for (int h = 0; h < 2; ++h) off[h] = ((uint32_t)row0 + r) * 128u + 16u * ((4u * h + g) ^ s);
         } else {
-            const uint32_t G = (uint32_t)lane >> 4, s = (uint32_t)lane & 15, kk = 8u * (G >> 1) + (s >> 2);
+            // (rows 32 H + 4 e on exchange the same way)
+            const uint32_t kk = 8u * g + (r >> 2);
 #pragma unroll
             for (int c = 0; c < C; ++c)
-                off[c] = kk * (2u * T) + 64u * (((uint32_t)row0 / 32u + c) ^ mn_swizzle<T>(kk)) + 32u * (G & 1) + 8u * (s & 3);
+                off[c] = kk * (2u * T) + 32u * (((uint32_t)row0 / 16u + c) ^ mn_swizzle<T>(kk)) + 8u * (r & 3);
         }
     }
     // Read Q of the step in half H of a pair.
     template <int H, int Q>
-    __device__ __forceinline__ void read(i32x4 (&f)[C][2], const uint8_t *panel) const
+    __device__ __forceinline__ void read(i32x4 (&f)[C], const uint8_t *panel) const
     {
         if constexpr (KM) {
-            constexpr int c = Q / 2, h = Q % 2;
-            f[c][h] = *reinterpret_cast<const i32x4 *>(panel + off[2 * H + h] + 4096 * c);
+            f[Q] = *reinterpret_cast<const i32x4 *>(panel + off[H] + 2048 * Q);
         } else {
-            constexpr int c = Q / 4, h = (Q / 2) % 2, e = Q % 2;
-            const uint8_t *p = panel + off[c] + (32 * H + 16 * h + 4 * e) * 2 * T;
+            constexpr int c = Q / 2, e = Q % 2;
+            const uint8_t *p = panel + off[c] + (32 * H + 4 * e) * 2 * T;
             const auto x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(lds_void *)p);
             const i32x2_t u = __builtin_bit_cast(i32x2_t, x);
             if constexpr (e == 0) {
-                f[c][h].x = u.x;
-                f[c][h].y = u.y;
+                f[c].x = u.x;
+                f[c].y = u.y;
             } else {
-                f[c][h].z = u.x;
-                f[c][h].w = u.y;
+                f[c].z = u.x;
+                f[c].w = u.y;
             }
         }
     }
@@ -159,7 +186,7 @@ struct Reader {
 
 template <int MI, int NB>
 struct Frag {
-    i32x4 a[MI][2], b[NB][2];
+    i32x4 a[2 * MI], b[2 * NB];
 };
 
 // The ring of a tile and the K loop over it: NA slots for A panels, NB_ for
@@ -175,16 +202,16 @@ struct Tile {
     static constexpr int kStage = kRing / 4 & ~15;          // epilogue staging bytes of a wave
     typedef Loader<AK, TM> LA;
     typedef Loader<BK, TN> LB;
-    static constexpr int kM = 2 * MI * NB;                  // MFMAs of a step
-    Reader<AK, TM, MI> ra;
-    Reader<BK, TN, NB> rb;
-    static constexpr int kR = Reader<AK, TM, MI>::kReads + Reader<BK, TN, NB>::kReads;
+    static constexpr int kM = 4 * MI * NB;                  // MFMAs of a step
+    Reader<AK, TM, 2 * MI> ra;
+    Reader<BK, TN, 2 * NB> rb;
+    static constexpr int kR = Reader<AK, TM, 2 * MI>::kReads + Reader<BK, TN, 2 * NB>::kReads;
     static constexpr int kRSpan = kM * 3 / 4 > 0 ? kM * 3 / 4 : 1;
 
     template <int H, int Q>
     __device__ __forceinline__ void read1(Frag<MI, NB> &f, const uint8_t *pa, const uint8_t *pb) const
     {
-        constexpr int RA = Reader<AK, TM, MI>::kReads;
+        constexpr int RA = Reader<AK, TM, 2 * MI>::kReads;
         if constexpr (Q < RA) ra.template read<H, Q>(f.a, pa);
         else rb.template read<H, Q - RA>(f.b, pb);
     }
@@ -195,11 +222,25 @@ struct Tile {
         if constexpr (WA && Q < LA::L) la.template load<Q>(pa, w);
         else lb.template load<Q - (WA ? LA::L : 0)>(pb, w);
     }
+    template <bool WA, int Q>
+    __device__ __forceinline__ uint32_t prepare1(const LA &la, const LB &lb, uint8_t *pa, uint8_t *pb, int w) const
+    {
+        if constexpr (WA && Q < LA::L) return la.template prepare<Q>(pa, w);
+        else return lb.template prepare<Q - (WA ? LA::L : 0)>(pb, w);
+    }
+    template <bool WA, int Q>
+    __device__ __forceinline__ void issue1(const LA &la, const LB &lb, uint32_t voff) const
+    {
+        if constexpr (WA && Q < LA::L) la.issue(voff);
+        else lb.issue(voff);
+    }
 
     // One step: MFMAs on cur, fragments of the next step (of panels ra_, rb_)
-    // into nxt, and loads into the panels pa and pb.
+    // into nxt, and loads into the panels pa and pb.  An MFMA of 16 cycles
+    // covers about three other instructions, so reads and loads are dealt out
+    // one by one, and a load's address part goes one MFMA ahead of it.
     template <bool ODD, class Seek>
-    __device__ __forceinline__ void step(f32x16 (&acc)[MI][NB], Frag<MI, NB> &cur, Frag<MI, NB> &nxt, LA &la, LB &lb,
+    __device__ __forceinline__ void step(f32x4 (&acc)[2 * MI][2 * NB], Frag<MI, NB> &cur, Frag<MI, NB> &nxt, LA &la, LB &lb,
                                          const uint8_t *ra_, const uint8_t *rb_, uint8_t *pa, uint8_t *pb, int w, Seek &&seek)
     {
         constexpr bool WA = ODD, WB = ODD != STAG;
@@ -215,17 +256,24 @@ struct Tile {
             seek();                  // aim at the pair that this step and the next one load
         }
         __builtin_amdgcn_sched_barrier(0);
+        uint32_t voff = 0;
         static_for<kM>([&](auto mm) {
-            constexpr int m = decltype(mm)::value, S = m / (MI * NB), i = (m % (MI * NB)) / NB, j = m % NB;
-            acc[i][j] = mfma32<IN>(cur.b[j][S], cur.a[i][S], acc[i][j]);
+            constexpr int m = decltype(mm)::value, i = m / (2 * NB), j = m % (2 * NB);
+            mfma_into<IN>(acc[i][j], cur.b[j], cur.a[i]);
             if constexpr (m < kRSpan) {
                 static_for<(kR * (m + 1)) / kRSpan - (kR * m) / kRSpan>([&](auto rr) {
                     read1<ODD ? 0 : 1, (kR * m) / kRSpan + decltype(rr)::value>(nxt, ra_, rb_);
                 });
             }
-            static_for<(L * (m + 1)) / kM - (L * m) / kM>([&](auto ll) {
-                load1<WA, (L * m) / kM + decltype(ll)::value>(la, lb, pa, pb, w);
-            });
+            if constexpr (L > 0 && kM >= 2 * L) {
+                constexpr int P = kM / (L > 0 ? L : 1), q = m / P;
+                if constexpr (q < L && m % P == 0) voff = prepare1<WA, q>(la, lb, pa, pb, w);
+                if constexpr (q < L && m % P == 1) issue1<WA, q>(la, lb, voff);
+            } else {
+                static_for<(L * (m + 1)) / kM - (L * m) / kM>([&](auto ll) {
+                    load1<WA, (L * m) / kM + decltype(ll)::value>(la, lb, pa, pb, w);
+                });
+            }
             __builtin_amdgcn_sched_barrier(0);
         });
     }
@@ -234,15 +282,13 @@ struct Tile {
     // which past the last one has to read nothing.  The loop body is one block
     // without branches and runs at least once.
     template <class Seek>
-    __device__ __forceinline__ void run(f32x16 (&acc)[MI][NB], uint8_t *ring, LA &la, LB &lb, int np, Seek &&seek)
+    __device__ __forceinline__ void run(f32x4 (&acc)[2 * MI][2 * NB], uint8_t *ring, LA &la, LB &lb, int np, Seek &&seek)
     {
         const int lane = threadIdx.x & 63, w = wave_id();
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
+        for (int i = 0; i < 2 * MI; ++i)
 #pragma unroll
-            for (int j = 0; j < NB; ++j)
-#pragma unroll
-                for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+            for (int j = 0; j < 2 * NB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         ra.init(32 * MI * (w >> 1), lane);
         rb.init(32 * NB * (w & 1), lane);
         uint8_t *const ringb = ring + NA * kA;
@@ -268,6 +314,7 @@ struct Tile {
             a = a1;
             b = b1;
         } while (++pair < np);
+        asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
         s_wait_vm<0>();
         s_wait_lgkm0();
         __builtin_amdgcn_s_barrier();       // the ring is free: the epilogue stages in it
@@ -384,31 +431,30 @@ __device__ __forceinline__ SplitTile tile_of_block(uint32_t b, uint32_t mt, uint
     else return {tile_at(b, mt, nt), 0};
 }
 
-// Holds a row of accumulator blocks in their AGPRs up to here: the compiler
+// Holds two rows of accumulator blocks in their AGPRs up to here: the compiler
 // otherwise reads all 256 at the end of the K loop and spills the fragments.
-template <int NB>
-__device__ __forceinline__ void pin(f32x16 (&acc)[NB])
+template <int N>
+__device__ __forceinline__ void pin(f32x4 (&r0)[N], f32x4 (&r1)[N])
 {
 #pragma unroll
-    for (int j = 0; j < NB; ++j) asm volatile("" : "+a"(acc[j]));
+    for (int j = 0; j < N; ++j) asm volatile("" : "+a"(r0[j]), "+a"(r1[j]));
 }
 
 // Epilogue: a 32-row block of a wave's quadrant goes through LDS, so that
-// whole row segments are stored.  stage_block writes value(j, q), the four
-// columns 32j + 8q + 4g .. + 3 of this lane's row, W blocks of 32 columns;
+// whole row segments are stored.  stage_block writes value(h, j), the four
+// columns 16j + 4g .. + 3 of row 16h + l%16 (lane l, g = l/16), W times 32 columns;
 // flush_block stores the staged rows at dst (row r at dst + r row_bytes),
 // `rows` of which exist, `col_bytes` of each.
 template <int DT, int W, class F>
 __device__ __forceinline__ void stage_block(uint8_t *reg, int lane, F &&value)
 {
-    constexpr int ES = es_of<DT>();
-    uint8_t *row = reg + (lane & 31) * StageGeom<ES, W>::RBP + 4 * (lane >> 5) * ES;
-    static_for<W>([&](auto jj) {
-        constexpr int j = decltype(jj)::value;
-        static_for<4>([&](auto qq) {
-            constexpr int q = decltype(qq)::value;
-            const float4 x = value(jj, qq);
-            *reinterpret_cast<typename Quad<ES>::T *>(row + (32 * j + 8 * q) * ES) = pack_quad<DT>(x.x, x.y, x.z, x.w);
+    constexpr int ES = es_of<DT>(), RBP = StageGeom<ES, W>::RBP;
+    uint8_t *row = reg + (lane & 15) * RBP + 4 * (lane >> 4) * ES;
+    static_for<2>([&](auto hh) {
+        static_for<2 * W>([&](auto jj) {
+            const float4 x = value(hh, jj);
+            *reinterpret_cast<typename Quad<ES>::T *>(row + 16 * decltype(hh)::value * RBP + 16 * decltype(jj)::value * ES) =
+                pack_quad<DT>(x.x, x.y, x.z, x.w);
         });
     });
 }
@@ -437,16 +483,16 @@ __device__ __forceinline__ void flush_block(const uint8_t *reg, void *dst, uint3
 
 // The raw sums of W accumulator blocks from block column J0 on, to dst (row
 // stride ld floats): a split's part of the workspace.
-template <int W, int J0, int MI, int NB>
-__device__ __forceinline__ void put_sums(f32x16 (&acc)[MI][NB], uint8_t *reg, float *dst, int64_t ld, int rows, int cols, int lane)
+template <int W, int J0, int M2, int N2>
+__device__ __forceinline__ void put_sums(f32x4 (&acc)[M2][N2], uint8_t *reg, float *dst, int64_t ld, int rows, int cols, int lane)
 {
-    static_for<MI>([&](auto ii) {
+    static_for<M2 / 2>([&](auto ii) {
         constexpr int i = decltype(ii)::value;
         __builtin_amdgcn_sched_barrier(0);
-        pin(acc[i]);
-        stage_block<DT_F32, W>(reg, lane, [&](auto jj, auto qq) {
-            constexpr int j = J0 + decltype(jj)::value, q = decltype(qq)::value;
-            return make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+        pin(acc[2 * i], acc[2 * i + 1]);
+        stage_block<DT_F32, W>(reg, lane, [&](auto hh, auto jj) {
+            const f32x4 x = acc[2 * i + decltype(hh)::value][2 * J0 + decltype(jj)::value];
+            return make_float4(x[0], x[1], x[2], x[3]);
         });
         flush_block<4, W, false>(reg, dst + 32 * i * ld, (uint32_t)(4 * ld), rows - 32 * i, 4 * cols, lane);
     });
