@@ -22,8 +22,10 @@
 // MFMAs.  The fragments of the next step are read between the MFMAs too.
 //
 // k-major panel (rows of K): row r at 128 r, its 16-byte chunk c at position
-// c ^ s(r), s(r) = (r%8) ^ ((r/8)%2), so that the 16 lanes that a 128-bit
-// read serves at once cover all 64 banks.
+// c ^ s(r), s(r) = (r%8) ^ ((r/4)%2).  A 128-bit read of 16 rows and 4 chunks
+// is served 16 lanes at a time, of each 32 lanes 0-3, 12-15, 20-23 and 24-27
+// and then the others (the bank conflict counter tells: without the second
+// term 0.5 conflicts a read, with it none), and s puts those on all 64 banks.
 // mn-major panel (16-bit; rows of M or N at each K): K row kk at (2 T) kk, its
 // 32-byte block b at b ^ x(kk).  The transposing read (ds_read_b64_tr_b16)
 // takes 32 bytes from each of 4 consecutive K rows in a 16-lane group, and
@@ -63,6 +65,7 @@ __device__ __forceinline__ int pairs_of(int64_t kbytes) { return kbytes > 128 ? 
 // Readable bytes as a buffer resource takes them.
 __device__ __forceinline__ uint32_t clamp_bytes(int64_t b) { return b <= 0 ? 0u : (b < 0x7FFFFFFF ? (uint32_t)b : 0x7FFFFFFFu); }
 
+__device__ __forceinline__ uint32_t k_swizzle(uint32_t row) { return (row & 7) ^ (row >> 2 & 1); }
 template <int T>
 __device__ __forceinline__ uint32_t mn_swizzle(uint32_t kk)
 {
@@ -79,7 +82,7 @@ struct Loader {
     const uint8_t *base;
     int64_t bytes, step;
     i32x4 r;
-    uint32_t v[L], klimit, chunk[2], add[2];
+    uint32_t v[L], klimit, chunk, add;
 
     __device__ __forceinline__ void init_k(const uint8_t *b, int64_t n, int64_t ld, int64_t kbytes, int w, int lane)
     {
@@ -87,11 +90,10 @@ struct Loader {
         bytes = n;
         klimit = (uint32_t)kbytes;
         r = make_rsrc_words(base, clamp_bytes(bytes));
-        const uint32_t row = (uint32_t)lane >> 3, c = ((uint32_t)lane & 7) ^ row ^ ((uint32_t)(L * w) & 1);
-        chunk[0] = 16 * c;
-        chunk[1] = chunk[0] ^ 16;
+        const uint32_t row = (uint32_t)lane >> 3;
+        chunk = 16 * (((uint32_t)lane & 7) ^ k_swizzle(row));
 #pragma unroll
-        for (int q = 0; q < L; ++q) v[q] = (8 * q + row) * (uint32_t)ld + chunk[q & 1];
+        for (int q = 0; q < L; ++q) v[q] = (8 * q + row) * (uint32_t)ld + chunk;
     }
     __device__ __forceinline__ void init_mn(const uint8_t *b, int64_t n, int64_t ld, int64_t cols, int w, int lane)
     {
@@ -111,8 +113,7 @@ struct Loader {
     {
         if constexpr (KM) {
             const uint32_t kb = (uint32_t)pair * 128u;
-            add[0] = kb + chunk[0] < klimit ? kb : kOOB;
-            add[1] = kb + chunk[1] < klimit ? kb : kOOB;
+            add = kb + chunk < klimit ? kb : kOOB;
         } else {
             const int64_t off = (int64_t)pair * step;
             r = make_rsrc_words(base + off, clamp_bytes(bytes - off));
@@ -125,7 +126,7 @@ struct Loader {
     {
         const uint32_t m0 = (uint32_t)(uintptr_t)(lds_void *)(panel + 1024 * (L * w + Q));
         asm volatile("s_mov_b32 m0, %0" : : "s"(m0));
-        return v[Q] + (KM ? add[Q & 1] : 0u);
+        return v[Q] + (KM ? add : 0u);
     }
     __device__ __forceinline__ void issue(uint32_t voff) const
     {
@@ -150,10 +151,8 @@ struct Reader {
     {
         const uint32_t r = (uint32_t)lane & 15, g = (uint32_t)lane >> 4;
         if constexpr (KM) {
-            // 16 rows on, s(r) exchanges the same positions
-            const uint32_t s = (r & 7) ^ (r >> 3);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) off[h] = ((uint32_t)row0 + r) * 128u + 16u * ((4u * h + g) ^ s);
+            for (int h = 0; h < 2; ++h) off[h] = ((uint32_t)row0 + r) * 128u + 16u * ((4u * h + g) ^ k_swizzle(r));
         } else {
             // (rows 32 H + 4 e on exchange the same way)
             const uint32_t kk = 8u * g + (r >> 2);
@@ -258,7 +257,8 @@ struct Tile {
         __builtin_amdgcn_sched_barrier(0);
         uint32_t voff = 0;
         static_for<kM>([&](auto mm) {
-            constexpr int m = decltype(mm)::value, i = m / (2 * NB), j = m % (2 * NB);
+            // columns back and forth, so that neighbours share an operand (0.5%)
+            constexpr int m = decltype(mm)::value, i = m / (2 * NB), c = m % (2 * NB), j = i % 2 ? 2 * NB - 1 - c : c;
             mfma_into<IN>(acc[i][j], cur.b[j], cur.a[i]);
             if constexpr (m < kRSpan) {
                 static_for<(kR * (m + 1)) / kRSpan - (kR * m) / kRSpan>([&](auto rr) {
