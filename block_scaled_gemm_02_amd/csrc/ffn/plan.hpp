@@ -18,26 +18,27 @@ struct Plan {
 
 // The cheapest plan of a rows x cols product over kbytes of K by an estimate
 // in microseconds, from times measured on the card (256 compute units):
-//   * a pair of 128 bytes of K takes a Big tile 1.03 us while at most 128 tiles
-//     are at work (2048 cycles of MFMA) and 1.5 us at 256 (the clock falls
-//     under the power limit); a Mid tile 0.35 and 0.485 us, a Small one 0.28
-//     and 0.31 us, whatever its MFMAs: the loads bound those;
-//   * launch, first loads and epilogue: 6, 5.5 and 4.5 us, and 4, 3 and 1.5 us
-//     for each further round of 256 tiles;
-//   * the operands come from memory at 4.9 TB/s;
-//   * splitting K (few tiles, long K) costs 3.5 us for the second kernel and
-//     the partial sums' way to memory and back at 2.5 TB/s of them.
-// Measured against it (us, Big / Mid / Small / Mid split in 4): 67 x 4096,
-// K 7168 int8: 63.3 / 23.7 / 19.9 / 13.3; 300 x 1000, K 1504 int8: 20.5 / 11.0
-// / 7.9 / 10.3; 512 x 4096, K 4096 int8: 39.8 / 17.1 / 14.2 / 25.1; 1000 x
-// 4096, K 4096 bf16: 70.7 / 38.1 / 44.3; 2048 x 8192, K 4096 int8: 62.3 / 82.3
-// / 95.2.
+//   * a pair of 128 bytes of K takes a Big tile 0.93 us while at most 128 tiles
+//     are at work (2048 cycles of MFMA) and 1.41 us at 256 (the clock falls
+//     under the power limit); a Mid tile 0.32 and 0.41 us, a Small one 0.25
+//     and 0.30 us, whatever its MFMAs: the loads bound those;
+//   * launch, first loads and epilogue: 9.5, 6.5 and 4.4 us, and 4, 3 and 0.75
+//     us for each further round of 256 tiles (two Small ones overlap on a CU);
+//   * the operands come from memory at 4.9 TB/s (and 3.5 us of launch);
+//   * splitting K (few tiles, long K) costs 1.5 us (a second kernel, less the
+//     epilogue) and the partial sums' way to memory and back at 2.2 TB/s of them.
+// Measured against it (us, Big / Mid / Small / Mid with K in parts): 67 x 4096,
+// K 7168 int8: 62.1 / 23.6 / 18.4 / 13.3 (4 parts); 512 x 4096, K 4096 int8:
+// 39.4 / 16.5 / 13.7 / 17.9 (2); gated fp16 509 x 2048, K 7168: 114 / 44.9 /
+// 38.9 / 43.5 (2); gated bf16 2000 x 2048, K 4096: 71.1 / 63.6 / 78.1;
+// 2048 x 8192, K 4096 int8: 54.7 / 73.8 / 85.9; 6000 x 704, K 512 int8: 12.3 /
+// 10.8 / 9.0.
 struct ShapeCost {
     int tm, tn;
     double fixed, round, pair, pair_all;
 };
 static constexpr ShapeCost kShapeCost[3] = {
-    {256, 256, 6.0, 4.0, 1.03, 1.5}, {128, 128, 5.5, 3.0, 0.35, 0.485}, {64, 128, 4.5, 1.5, 0.28, 0.31}};
+    {256, 256, 9.5, 4.0, 0.93, 1.41}, {128, 128, 6.5, 3.0, 0.32, 0.41}, {64, 128, 4.4, 0.75, 0.25, 0.30}};
 
 inline int64_t pairs_in(int64_t kbytes) { return kbytes > 128 ? (kbytes + 127) / 128 : 1; }
 
@@ -49,8 +50,8 @@ inline Plan plan_with(int shape, int splits, int64_t rows, int64_t cols, int64_t
     const double part = rest > 128 ? c.pair + (c.pair_all - c.pair) * (double)(rest - 128) / 128 : c.pair;
     double t = c.fixed + (double)(full + (rest > 0) - 1) * c.round +
                (double)((pairs_in(kbytes) + splits - 1) / splits) * ((double)full * c.pair_all + (rest ? part : 0));
-    t = std::max(t, c.fixed + (double)(rows + cols) * (double)kbytes / 4.9e6);
-    if (splits > 1) t += 3.5 + (double)rows * (double)cols * splits * 4 / 2.5e6;
+    t = std::max(t, 3.5 + (double)(rows + cols) * (double)kbytes / 4.9e6);
+    if (splits > 1) t += 1.5 + (double)rows * (double)cols * splits * 4 / 2.2e6;
     return {shape, splits, (int)mt, (int)nt, t};
 }
 
