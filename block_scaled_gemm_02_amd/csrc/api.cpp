@@ -766,6 +766,7 @@ int bsg_validate_gemm_glu_bwd(const void *dh, const void *x, const void *w_gate,
     if (!is_16bit(dtype)) return fail(BSG_ERR_DTYPE, "dtype %d is not fp16 or bf16", dtype);
     if (n % 8 || k % 8)
         return fail(BSG_ERR_ALIGN, "N=%lld and K=%lld must be multiples of 8", (long long)n, (long long)k);
+    if (int r = check_ffn_tiles(m, n)) return r;       // the element-wise pass: fewer than 2^32 threads
     if (int r = check_ffn_tiles(m, k)) return r;
     if (int r = check_ffn_tiles(2 * n, k)) return r;
     if (!dw_gate != !dw_up) return fail(BSG_ERR_NULLPTR, "dw_gate and dw_up are given together or not at all");

@@ -9,7 +9,7 @@ namespace bsg {
 namespace ffn {
 
 struct Plan {
-    int shape;      // 0: Big (256 x 256), 1: Mid (128 x 128), 2: Small (64 x 128)
+    int shape;      // 0: Big (256 x 256), 1: Mid (128 x 128), 2: Small (64 x 128), 3: Shared (128 x 128)
     int splits;     // parts of K (Mid only; 1: whole)
     int mt, nt;     // tiles
     double us;      // the estimate
@@ -20,25 +20,29 @@ struct Plan {
 // in microseconds, from times measured on the card (256 compute units):
 //   * a pair of 128 bytes of K takes a Big tile 0.93 us while at most 128 tiles
 //     are at work (2048 cycles of MFMA) and 1.41 us at 256 (the clock falls
-//     under the power limit); a Mid tile 0.32 and 0.41 us, a Small one 0.25
-//     and 0.30 us, whatever its MFMAs: the loads bound those;
-//   * launch, first loads and epilogue: 9.5, 6.5 and 4.4 us, and 4, 3 and 0.75
-//     us for each further round of 256 tiles (two Small ones overlap on a CU);
+//     under the power limit); a Mid tile 0.36 and 0.47 us, a Shared one 0.38
+//     and 0.48 us, a Small one 0.27 and 0.32 us, whatever its MFMAs: the loads
+//     bound those;
+//   * launch, first loads and epilogue: 9.5 (Big), 5.0 (Mid), 4.2 (Small) and 4.5
+//     us (Shared), and 4, 4, 0.75 and 0.75 us for each further round of 256
+//     tiles: two Small or Shared ones overlap on a CU, and Shared is meant for
+//     products that have them;
 //   * the operands come from memory at 4.9 TB/s (and 3.5 us of launch);
 //   * splitting K (few tiles, long K) costs 1.5 us (a second kernel, less the
 //     epilogue) and the partial sums' way to memory and back at 2.2 TB/s of them.
-// Measured against it (us, Big / Mid / Small / Mid with K in parts): 67 x 4096,
-// K 7168 int8: 62.1 / 23.6 / 18.4 / 13.3 (4 parts); 512 x 4096, K 4096 int8:
-// 39.4 / 16.5 / 13.7 / 17.9 (2); gated fp16 509 x 2048, K 7168: 114 / 44.9 /
-// 38.9 / 43.5 (2); gated bf16 2000 x 2048, K 4096: 71.1 / 63.6 / 78.1;
-// 2048 x 8192, K 4096 int8: 54.7 / 73.8 / 85.9; 6000 x 704, K 512 int8: 12.3 /
-// 10.8 / 9.0.
+// Measured (us, Big / Mid / Small / Shared / Mid with K in parts): 67 x 4096, K
+// 7168 int8: 62.1 / 23.6 / 18.4 / - / 13.3 (4 parts); 512 x 4096, K 4096 int8:
+// 39.4 / 16.5 / 13.7 / - / 17.9 (2); 1600 x 2048, K 7168 int8: - / 29.8 / 35.7
+// / 31.9; gated fp16 509 x 2048, K 7168: 114 / 44.9 / 38.9 / - / 43.5 (2); gated
+// bf16 2000 x 2048, K 4096: 71.1 / 63.6 / 78.1 / 57.5; 2048 x 8192, K 4096 int8:
+// 54.9 / 73.8 / 85.9 / 63.9; 6000 x 704, K 512 int8: 12.4 / 10.8 / 9.0 / 7.6.
 struct ShapeCost {
     int tm, tn;
     double fixed, round, pair, pair_all;
 };
-static constexpr ShapeCost kShapeCost[3] = {
-    {256, 256, 9.5, 4.0, 0.93, 1.41}, {128, 128, 6.5, 3.0, 0.32, 0.41}, {64, 128, 4.4, 0.75, 0.25, 0.30}};
+static constexpr ShapeCost kShapeCost[4] = {
+    {256, 256, 9.5, 4.0, 0.93, 1.41}, {128, 128, 5.0, 4.0, 0.36, 0.47},
+    {64, 128, 4.2, 0.75, 0.27, 0.32}, {128, 128, 4.5, 0.75, 0.38, 0.48}};
 
 inline int64_t pairs_in(int64_t kbytes) { return kbytes > 128 ? (kbytes + 127) / 128 : 1; }
 
@@ -61,9 +65,9 @@ inline Plan plan_of(int64_t rows, int64_t cols, int64_t kbytes)
     auto offer = [&](const Plan &p) {
         if (p.us < best.us) best = p;
     };
-    for (int s = 1; s < 3; ++s) offer(plan_with(s, 1, rows, cols, kbytes));
-    // a split keeps at least four pairs, and splits never make more workgroups than two rounds
     const int64_t mid = ((rows + 127) / 128) * ((cols + 127) / 128), pairs = pairs_in(kbytes);
+    for (int s = 1; s < (mid > 256 ? 4 : 3); ++s) offer(plan_with(s, 1, rows, cols, kbytes));
+    // a split keeps at least four pairs, and splits never make more workgroups than two rounds
     for (int n = 2; n <= 8 && pairs >= 4 * n && mid * n <= 512; ++n) offer(plan_with(1, n, rows, cols, kbytes));
     return best;
 }
@@ -72,9 +76,9 @@ inline Plan plan_of(int64_t rows, int64_t cols, int64_t kbytes)
 // set both have one shape and no splits and go out as one launch, whose
 // workgroups fill the compute units that the last round of one of them alone
 // would leave idle.  Measured for the gradients of a gated block (us, two
-// launches / one): 1003 x 1408 x 2048 47.1 / 38.2, 256 x 512 x 1024 16.1 / 11.6,
-// 8192 x 1408 x 2048 225 / 207; 700 x 4096 x 1024, whose dX has few tiles and
-// long K, 51.3 (dX in parts) / 59.6.
+// launches / one): 1003 x 1408 x 2048 39.1 / 30.6, 256 x 512 x 1024 16.6 / 11.8,
+// 8192 x 1408 x 2048 204 / 177; 700 x 4096 x 1024, whose dX has few tiles and
+// long K, 44.1 (dX in parts) / 59.6.
 struct PlanPair {
     Plan x, w;
     bool together;
@@ -83,14 +87,16 @@ inline PlanPair plan_pair(int64_t xr, int64_t xc, int64_t xk, int64_t wr, int64_
 {
     PlanPair best{plan_of(xr, xc, xk), plan_of(wr, wc, wk), false};
     double least = best.x.us + best.w.us;
-    for (int s = 0; s < 3; ++s) {
+    for (int s = 0; s < 4; ++s) {
         const ShapeCost &c = kShapeCost[s];
         const Plan x = plan_with(s, 1, xr, xc, xk), w = plan_with(s, 1, wr, wc, wk);
         const double xt = (double)x.mt * x.nt, wt = (double)w.mt * w.nt, xp = (double)pairs_in(xk), wp = (double)pairs_in(wk);
-        // the longest tile among all the others (Small ones come to share
-        // a compute unit two by two), or the compute units kept busy to the end
-        const double share = s == 2 ? 1 + std::min(1.0, std::max(0.0, (xt + wt - 256) / 256)) : 1;
-        const double one = std::max(xp, wp) * (c.pair + c.pair_all) / 2 * share + c.fixed;
+        // the longest tile among all the others (a Small or Shared one comes to
+        // share its compute unit with a shorter one), or the compute units kept busy to the end
+        const double share = std::min(1.0, std::max(0.0, (xt + wt - 256) / 256));
+        if (s == 3 && share == 0) break;
+        const double one = c.fixed + (s < 2 ? std::max(xp, wp) * (c.pair + c.pair_all) / 2
+                                            : std::max(xp, wp) * c.pair + (c.round + std::min(xp, wp) * c.pair_all) * share);
         const double all = (xt * xp + wt * wp) / 256 * c.pair_all + c.fixed + c.round * ((xt + wt) / 256);
         const double t = std::max(one, all);
         if (t < least) {

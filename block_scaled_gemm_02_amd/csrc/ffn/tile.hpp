@@ -346,7 +346,13 @@ __device__ __forceinline__ void store4(void *p, int64_t i, float4 v)
 }
 
 // The tile shapes: Big for products with enough 256 x 256 tiles, the others
-// with more and smaller ones, whose rings hold more pairs.  Below Big the
+// with more and smaller ones.  Mid's ring holds four pairs, for a compute unit
+// that has one tile; Shared is the same tile on half the LDS, for products of
+// more than 256 of them: two workgroups share a compute unit and one's first
+// loads and epilogue hide behind the other (us, Mid / Shared: int8 2048 x 4096,
+// K 2048 24.3 / 20.5; gated bf16 2000 x 2048, K 4096 64.2 / 57.5; the gradients
+// of 1003 x 1408 x 2048 36.2 / 30.7; but int8 67 x 4096, K 7168 in 4 parts, one
+// workgroup a compute unit, 13.3 / 14.1).  Below Big the
 // loads bound the time, not the matrix cores: a CU's direct-to-LDS loads reach
 // about 50 bytes a cycle, 32 KB (Mid) or 24 KB (Small) a pair for 512 or 256
 // cycles of MFMA.  (Letting the four waves divide a pair's K instead of the
@@ -355,13 +361,14 @@ __device__ __forceinline__ void store4(void *p, int64_t i, float4 v)
 template <int MI_, int NB_, int SA, int SB>
 struct Shape {
     static constexpr int MI = MI_, NB = NB_, TM = 64 * MI, TN = 64 * NB;
-    static constexpr int kWaves = MI * NB == 16 ? 1 : 2;     // waves a SIMD that the registers allow
+    static constexpr int kWaves = 128 * (SA * TM + SB * TN) <= 80 * 1024 ? 2 : 1;    // waves a SIMD, by the LDS
     template <int IN, bool AK, bool BK>
     using Of = Tile<IN, AK, BK, MI, NB, SA, SB>;
 };
 typedef Shape<4, 4, 2, 3> Big;
 typedef Shape<2, 2, 4, 4> Mid;
 typedef Shape<1, 2, 3, 3> Small;
+typedef Shape<2, 2, 2, 3> Shared;
 
 // K divided over workgroups, where a product has fewer tiles than the card
 // has compute units: split s of `splits` sums the pairs [first, first + count)
@@ -384,6 +391,7 @@ void with_shape(const Plan &p, F &&f)
 {
     if (p.shape == 0) f(Big{}, std::false_type{});
     else if (p.shape == 2) f(Small{}, std::false_type{});
+    else if (p.shape == 3) f(Shared{}, std::false_type{});
     else if (p.splits == 1) f(Mid{}, std::false_type{});
     else f(Mid{}, std::true_type{});
 }

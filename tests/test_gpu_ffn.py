@@ -320,6 +320,44 @@ def test_gemm_glu_bwd_small_integers_are_exact(m, n, k):
     assert torch.equal(dwg, (dg.t() @ x.double()).to(BF)) and torch.equal(dwu, (du.t() @ x.double()).to(BF))
 
 
+@pytest.mark.parametrize("m,n,k", [(1001, 2120, 520), (2900, 712, 208)])
+def test_products_of_many_middle_tiles(m, n, k):
+    """More than 256 tiles of 128 x 128 with ragged edges, where two workgroups
+    share a compute unit: exact sums of small integers in every operator."""
+    say("many middle tiles", m, n, k)
+    g = gen(n)
+    a, b = ints(g, m, 2 * k, lo=-2, hi=2), ints(g, 2 * n, 2 * k, lo=-2, hi=2)
+    one = torch.ones(max(m, 2 * n), device=DEV)
+    assert torch.equal(run_i8(a, b, one[:m], one[:2 * n], None, F32), (a.double() @ b.double().t()).float())
+    h, intact = guarded(m, n, BF)
+    bsg.gemm_glu_i8(a, b[:n], b[n:], one[:m], one[:n], one[:n], h, m, n, 2 * k, act="relu",
+                    workspace=scratch("gemm_glu_i8", m, n, 2 * k))
+    intact()
+    gr, ur = a.double() @ b[:n].double().t(), a.double() @ b[n:].double().t()
+    assert torch.equal(h, (gr.clamp(min=0) * ur).float().to(BF))
+    for dt in (BF, HF):
+        x, wg, wu = a[:, :k].to(dt).contiguous(), b[:n, :k].to(dt).contiguous(), b[n:, :k].to(dt).contiguous()
+        gr, ur = x.double() @ wg.double().t(), x.double() @ wu.double().t()
+        t = run_glu(x, wg, wu, "relu", True)
+        assert torch.equal(t[1], gr.to(dt)) and torch.equal(t[2], ur.to(dt))
+        assert torch.equal(t[0].double(), (gr.clamp(min=0) * ur).float().to(dt).double())
+
+
+@pytest.mark.parametrize("m,n,k", [(1001, 1416, 2056)])
+def test_gemm_glu_bwd_of_many_middle_tiles(m, n, k):
+    """The gradients on the same tiles, in one launch: ReLU and small integers,
+    so that every sum is exact."""
+    say("bwd many middle tiles", m, n, k)
+    g = gen(n)
+    for dt in (BF, HF):
+        dh, x, wg, wu, gg, uu = (ints(g, *s, lo=-2, hi=2, dt=dt) for s in ((m, n), (m, k), (n, k), (n, k), (m, n), (m, n)))
+        dx, dwg, dwu = run_bwd(dh, x, wg, wu, gg, uu, "relu")
+        on = (gg > 0).double()
+        dg, du = dh.double() * uu.double() * on, dh.double() * gg.double() * on
+        assert torch.equal(dx, (dg @ wg.double() + du @ wu.double()).to(dt))
+        assert torch.equal(dwg, (dg.t() @ x.double()).to(dt)) and torch.equal(dwu, (du.t() @ x.double()).to(dt))
+
+
 @pytest.mark.parametrize("kind", R.ACTS)
 def test_gemm_glu_bwd_matches_differences(kind):
     """dX and dWg, dWu against central differences of sum(dH * H) in 64 bits.
