@@ -1,4 +1,10 @@
 // gemm_i8: C = (A B^T) * a_scale * b_scale + bias from 8-bit integers.
+//
+// int32 sums; each is converted to fp32, which rounds it to 24 bits, only to
+// meet its scales, and C is rounded once more to its type.  8192^3 runs in
+// 379-389 us, 2830-2900 TOPS, the matrix cores 75% busy at the clock that the
+// power limit leaves (on zeros 280 us); 67 x 4096, K 7168 in 4 parts in 13.2
+// us, 11.2 of them the tiles, whose loads into LDS bound them.
 #include "few.hpp"
 
 namespace bsg {
