@@ -97,6 +97,15 @@ def test_gemm_glu_bwd_validation():
     assert L.bsg_validate_gemm_glu_bwd(*args[:-1], P + 8, need, 5, 64, 64, bsg.BF16, 0) == ALIGN
 
 
+def test_grids_past_the_launch_limit_are_refused():
+    """2^32 threads or 2^23 tiles: every product of sizes, and the backward's
+    element-wise pass over (m, n) where both of its products are small."""
+    m, n = 1 << 22, 1 << 20
+    assert i8(m=m, n=n) == UNSUP and glu(m=m, n=n) == UNSUP and glu_i8(m=m, n=n) == UNSUP
+    assert bwd(m=m, n=n, k=8) == UNSUP and bwd(m=m, n=8, k=1 << 20) == UNSUP and bwd(m=8, n=n, k=1 << 20) == UNSUP
+    assert bwd(m=m, n=8 * 64, k=8) == OK
+
+
 def test_workspace_bytes():
     for name in ("gemm_i8", "gemm_glu", "gemm_glu_i8", "gemm_glu_bwd"):
         assert bsg.workspace_bytes(name, 0, 0, 0) >= 0
