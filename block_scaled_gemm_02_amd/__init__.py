@@ -433,6 +433,8 @@ def workspace_bytes(name, m, n, k) -> int:
 
 
 _TORCH_OF = {F32: torch.float32, F16: torch.float16, BF16: torch.bfloat16}
+# (looked up once: an attribute of the torch module costs 50 ns a call)
+_I8, _F32, _current_device = torch.int8, torch.float32, torch._C._cuda_getDevice
 
 
 def _code(dtype, t) -> int:
@@ -443,10 +445,10 @@ def _code(dtype, t) -> int:
 
 
 def _addresses(*specs):
-    """The addresses of several (tensor, name, bytes, torch dtype), checked as
-    _need does.  A call for one token takes a few microseconds, and this one
-    pass of quick checks takes one; what does not pass them goes to _need,
-    which says what is wrong."""
+    """The addresses of several (tensor, name, bytes, torch dtype or None),
+    checked as _need does.  A call for one token takes a few microseconds, and
+    this one pass of quick checks takes one; what does not pass them goes to
+    _need, which says what is wrong."""
     dev, out = None, []
     for t, name, nbytes, dt in specs:
         if t is None or type(t) is int:
@@ -454,8 +456,8 @@ def _addresses(*specs):
             continue
         d = t.get_device()
         if dev is None and d >= 0:
-            dev = torch._C._cuda_getDevice()
-        if d != dev or t.dtype is not dt or t.nbytes < nbytes or not t.is_contiguous():
+            dev = _current_device()
+        if d != dev or (dt is not None and t.dtype is not dt) or t.nbytes < nbytes or not t.is_contiguous():
             _need(t, name, nbytes, dt)
         out.append(t.data_ptr())
     return out
@@ -467,21 +469,21 @@ def _act(act) -> int:
     return _ACTS[act]
 
 
-def _ws(workspace, name, m, n, k):
-    """(address, bytes) of a workspace; a plain address is taken to be large enough."""
+def _ws_bytes(workspace, name, m, n, k):
+    """Bytes of a workspace; a plain address is taken to be large enough."""
     if workspace is None:
-        return None, 0
+        return 0
     if isinstance(workspace, int):
-        return workspace, lib().bsg_workspace_bytes(_WS_OPS[name], m, n, k)
-    return _addresses((workspace, "workspace", 0, workspace.dtype))[0], workspace.nbytes
+        return lib().bsg_workspace_bytes(_WS_OPS[name], m, n, k)
+    return workspace.nbytes
 
 
 def quant_i8(x, q, scale, m, k, x_dtype=None, stream=None, validate_only=False):
     """Rows of x (m, k) -> 8-bit integers q and one fp32 scale a row (see
     include/bsg.h).  x_dtype: torch.float32 / float16 / bfloat16, from x if None."""
     xd = _code(x_dtype, x)
-    args = _addresses((x, "x", _out_bytes(xd, m * k), _TORCH_OF.get(xd)), (q, "q", m * k, torch.int8),
-                      (scale, "scale", 4 * m, torch.float32))
+    args = _addresses((x, "x", _out_bytes(xd, m * k), _TORCH_OF.get(xd)), (q, "q", m * k, _I8),
+                      (scale, "scale", 4 * m, _F32))
     args += (m, k, xd)
     if validate_only:
         return lib().bsg_validate_quant_i8(*args)
@@ -494,10 +496,11 @@ def gemm_i8(a, b, a_scale, b_scale, bias, c, m, n, k, bias_dtype=None, c_dtype=N
     (see include/bsg.h).  bias may be None."""
     cd = _code(c_dtype, c)
     bd = F32 if bias is None else _code(bias_dtype, bias)
-    args = _addresses((a, "a", m * k, torch.int8), (b, "b", n * k, torch.int8), (a_scale, "a_scale", 4 * m, torch.float32),
-                      (b_scale, "b_scale", 4 * n, torch.float32), (bias, "bias", _out_bytes(bd, n), _TORCH_OF.get(bd)),
-                      (c, "c", _out_bytes(cd, m * n), _TORCH_OF.get(cd)))
-    args += (*_ws(workspace, "gemm_i8", m, n, k), m, n, k, bd, cd)
+    args = _addresses((a, "a", m * k, _I8), (b, "b", n * k, _I8), (a_scale, "a_scale", 4 * m, _F32),
+                      (b_scale, "b_scale", 4 * n, _F32), (bias, "bias", _out_bytes(bd, n), _TORCH_OF.get(bd)),
+                      (c, "c", _out_bytes(cd, m * n), _TORCH_OF.get(cd)),
+                      (workspace, "workspace", 0, None))
+    args += (_ws_bytes(workspace, "gemm_i8", m, n, k), m, n, k, bd, cd)
     if validate_only:
         return lib().bsg_validate_gemm_i8(*args)
     _check(lib().gemm_i8(*args, _stream(stream)))
@@ -511,8 +514,9 @@ def gemm_glu(x, w_gate, w_up, h, g, u, m, n, k, act="silu", dtype=None, workspac
     dt = _code(dtype, x)
     mn, nk, td = _out_bytes(dt, m * n), _out_bytes(dt, n * k), _TORCH_OF.get(dt)
     args = _addresses((x, "x", _out_bytes(dt, m * k), td), (w_gate, "w_gate", nk, td), (w_up, "w_up", nk, td),
-                      (h, "h", mn, td), (g, "g", mn, td), (u, "u", mn, td))
-    args += (*_ws(workspace, "gemm_glu", m, n, k), m, n, k, dt, _act(act))
+                      (h, "h", mn, td), (g, "g", mn, td), (u, "u", mn, td),
+                      (workspace, "workspace", 0, None))
+    args += (_ws_bytes(workspace, "gemm_glu", m, n, k), m, n, k, dt, _act(act))
     if validate_only:
         return lib().bsg_validate_gemm_glu(*args)
     _check(lib().gemm_glu(*args, _stream(stream)))
@@ -522,11 +526,11 @@ def gemm_glu_i8(a, w_gate, w_up, a_scale, gate_scale, up_scale, h, m, n, k, act=
                 workspace=None, stream=None, validate_only=False):
     """gemm_glu from 8-bit integers and their scales (see include/bsg.h)."""
     dt = _code(h_dtype, h)
-    i8, f32 = torch.int8, torch.float32
-    args = _addresses((a, "a", m * k, i8), (w_gate, "w_gate", n * k, i8), (w_up, "w_up", n * k, i8),
-                      (a_scale, "a_scale", 4 * m, f32), (gate_scale, "gate_scale", 4 * n, f32),
-                      (up_scale, "up_scale", 4 * n, f32), (h, "h", _out_bytes(dt, m * n), _TORCH_OF.get(dt)))
-    args += (*_ws(workspace, "gemm_glu_i8", m, n, k), m, n, k, dt, _act(act))
+    args = _addresses((a, "a", m * k, _I8), (w_gate, "w_gate", n * k, _I8), (w_up, "w_up", n * k, _I8),
+                      (a_scale, "a_scale", 4 * m, _F32), (gate_scale, "gate_scale", 4 * n, _F32),
+                      (up_scale, "up_scale", 4 * n, _F32), (h, "h", _out_bytes(dt, m * n), _TORCH_OF.get(dt)),
+                      (workspace, "workspace", 0, None))
+    args += (_ws_bytes(workspace, "gemm_glu_i8", m, n, k), m, n, k, dt, _act(act))
     if validate_only:
         return lib().bsg_validate_gemm_glu_i8(*args)
     _check(lib().gemm_glu_i8(*args, _stream(stream)))
@@ -541,8 +545,8 @@ def gemm_glu_bwd(dh, x, w_gate, w_up, g, u, dx, dw_gate, dw_up, m, n, k, act="si
     td = _TORCH_OF.get(dt)
     args = _addresses((dh, "dh", mn, td), (x, "x", mk, td), (w_gate, "w_gate", nk, td), (w_up, "w_up", nk, td),
                       (g, "g", mn, td), (u, "u", mn, td), (dx, "dx", mk, td), (dw_gate, "dw_gate", nk, td),
-                      (dw_up, "dw_up", nk, td))
-    args += (*_ws(workspace, "gemm_glu_bwd", m, n, k), m, n, k, dt, _act(act))
+                      (dw_up, "dw_up", nk, td), (workspace, "workspace", 0, None))
+    args += (_ws_bytes(workspace, "gemm_glu_bwd", m, n, k), m, n, k, dt, _act(act))
     if validate_only:
         return lib().bsg_validate_gemm_glu_bwd(*args)
     _check(lib().gemm_glu_bwd(*args, _stream(stream)))
