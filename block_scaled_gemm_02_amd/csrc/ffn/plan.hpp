@@ -110,15 +110,17 @@ inline PlanPair plan_pair(int64_t xr, int64_t xc, int64_t xk, int64_t wr, int64_
 // The same estimate for the kernel of a few tokens (up to 64), cols weight
 // rows in all: the weights at 5.2 TB/s, and the tokens' rows, which every
 // workgroup of 16 weight rows reads from the L2 at 45 bytes a nanosecond and
-// compute unit (the first six hide behind the weights).  Measured, few / tiles
-// (us): 16 tokens of 4096 x 7168 int8 8.9 / 12; 32 tokens 12.1 / 12.1; gated
-// bf16 2048 x 7168, 16 tokens 15.1 / 18, 32 tokens 21.0 / 18; 8192 x 4096, 16
-// tokens 35.4 / 33.7; 512 x 512, 32 tokens 3.8 / 6.8.
+// compute unit (the first six hide behind the weights); the form for 33 to 64
+// tokens, with less of the weights in flight, takes 1.3 us more.  Measured, few
+// / tiles (us): int8 4096 x 7168, 16 tokens 8.6 / 11.2, 24 11.0 / 11.3, 40 15.3
+// / 11.8; int8 7168 x 2048, 24 tokens 7.2 / 8.0, 40 9.7 / 8.1; gated bf16 2048 x
+// 7168, 16 tokens 15.4 / 17.4, 24 18.7 / 17.5; gated bf16 8192 x 4096, 8 tokens
+// 28.7 / 33.5, 16 35.6 / 35.3; gated bf16 512 x 512, 64 tokens 4.6 / 5.1.
 inline bool few_is_cheaper(int64_t tokens, int64_t cols, int64_t kbytes)
 {
     if (tokens > 64) return false;
     const double rounds = (double)((cols + 4095) / 4096);
-    const double t = 2.5 + (double)cols * (double)kbytes / 5.2e6 +
+    const double t = (tokens > 32 ? 3.8 : 2.5) + (double)cols * (double)kbytes / 5.2e6 +
                      rounds * (double)std::max<int64_t>(0, tokens - 6) * (double)kbytes / 45000.0;
     return t <= plan_of(tokens, cols, kbytes).us;
 }
