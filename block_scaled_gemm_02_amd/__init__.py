@@ -166,9 +166,17 @@ def _grouped_common_need(padded_offsets, alpha, prob, m, num_experts):
     _need(prob, "prob", 4 * m, torch.float32)
 
 
+# The current device and its stream.  torch.cuda.current_stream() makes a Stream
+# object, 2.8 us a call; the queries beneath it are not public, and a torch
+# without GPU support lacks them: there the public functions answer.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or (lambda: torch.cuda.current_device())
+_raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+               or (lambda device: torch.cuda.current_stream(device).cuda_stream))
+
+
 def _stream(stream):
-    if stream is None:      # torch.cuda.current_stream().cuda_stream, without making a Stream object (2.8 us)
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    if stream is None:
+        return _raw_stream(_current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -434,7 +442,7 @@ def workspace_bytes(name, m, n, k) -> int:
 
 _TORCH_OF = {F32: torch.float32, F16: torch.float16, BF16: torch.bfloat16}
 # (looked up once: an attribute of the torch module costs 50 ns a call)
-_I8, _F32, _current_device = torch.int8, torch.float32, torch._C._cuda_getDevice
+_I8, _F32 = torch.int8, torch.float32
 
 
 def _code(dtype, t) -> int:
