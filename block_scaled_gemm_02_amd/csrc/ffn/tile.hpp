@@ -57,6 +57,24 @@ __device__ __forceinline__ void mfma_into(f32x4 &acc, const i32x4 &b, const i32x
     else asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
 }
 
+// mfma_into with a load of 16 bytes a lane into the LDS at dst + OFF + 16 lane.
+// One statement, so that nothing of the compiler's comes between M0, which holds
+// the LDS address, and the load; the MFMA is the wait state that the two need.
+template <int IN, int OFF>
+__device__ __forceinline__ void mfma_load(f32x4 &acc, const i32x4 &b, const i32x4 &a, const i32x4 &rsrc, uint8_t *dst, uint32_t voff)
+{
+    const uint32_t m0 = (uint32_t)(uintptr_t)(lds_void *)dst;
+    if constexpr (IN == IN_BF16)
+        asm volatile("s_add_u32 m0, %3, %6\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0\n\tbuffer_load_dwordx4 %4, %5, 0 offen lds"
+                     : "+a"(acc) : "v"(b), "v"(a), "s"(m0), "v"(voff), "s"(rsrc), "n"(OFF) : "memory", "m0", "scc");
+    else if constexpr (IN == IN_F16)
+        asm volatile("s_add_u32 m0, %3, %6\n\tv_mfma_f32_16x16x32_f16 %0, %1, %2, %0\n\tbuffer_load_dwordx4 %4, %5, 0 offen lds"
+                     : "+a"(acc) : "v"(b), "v"(a), "s"(m0), "v"(voff), "s"(rsrc), "n"(OFF) : "memory", "m0", "scc");
+    else
+        asm volatile("s_add_u32 m0, %3, %6\n\tv_mfma_i32_16x16x64_i8 %0, %1, %2, %0\n\tbuffer_load_dwordx4 %4, %5, 0 offen lds"
+                     : "+a"(acc) : "v"(b), "v"(a), "s"(m0), "v"(voff), "s"(rsrc), "n"(OFF) : "memory", "m0", "scc");
+}
+
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)); }
 
 // Pairs of a K extent in bytes; an empty sum runs one, of zeros.
@@ -119,26 +137,11 @@ struct Loader {
             r = make_rsrc_words(base + off, clamp_bytes(bytes - off));
         }
     }
-    // Load Q of the wave's share of the panel, in two parts that may stand
-    // apart (nothing else writes M0): its LDS address, and the load itself.
+    // Load Q of the wave's share of the panel: its offset in the tensor.  In the
+    // LDS it goes to 1024 Q past the wave's part.
     template <int Q>
-    __device__ __forceinline__ uint32_t prepare(uint8_t *panel, int w) const
-    {
-        const uint32_t m0 = (uint32_t)(uintptr_t)(lds_void *)(panel + 1024 * (L * w + Q));
-        asm volatile("s_mov_b32 m0, %0" : : "s"(m0));
-        return v[Q] + (KM ? add : 0u);
-    }
-    __device__ __forceinline__ void issue(uint32_t voff) const
-    {
-        asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(voff), "s"(r) : "memory");
-    }
-    template <int Q>
-    __device__ __forceinline__ void load(uint8_t *panel, int w) const
-    {
-        const uint32_t voff = prepare<Q>(panel, w);
-        asm volatile("s_nop 0");            // one wait state between M0 and the load that reads it
-        issue(voff);
-    }
+    __device__ __forceinline__ uint32_t offset() const { return v[Q] + (KM ? add : 0u); }
+    static __device__ __forceinline__ uint8_t *part(uint8_t *panel, int w) { return panel + 1024 * L * w; }
 };
 
 // Fragment reads of one wave from a panel: C blocks of 16 rows.
@@ -214,30 +217,40 @@ struct Tile {
         if constexpr (Q < RA) ra.template read<H, Q>(f.a, pa);
         else rb.template read<H, Q - RA>(f.b, pb);
     }
-    // Load Q of a step that loads A (WA) and / or B panels.
+    // Load Q of a step that loads A (WA) and / or B panels: its offset, and the
+    // load behind an MFMA, or by itself.
     template <bool WA, int Q>
+    __device__ __forceinline__ uint32_t offset1(const LA &la, const LB &lb) const
+    {
+        if constexpr (WA && Q < LA::L) return la.template offset<Q>();
+        else return lb.template offset<Q - (WA ? LA::L : 0)>();
+    }
+    template <bool WA, int Q>
+    __device__ __forceinline__ void mfma_load1(f32x4 &acc, const i32x4 &b, const i32x4 &a, const LA &la, const LB &lb, uint8_t *pa,
+                                               uint8_t *pb, int w, uint32_t voff) const
+    {
+        if constexpr (WA && Q < LA::L) mfma_load<IN, 1024 * Q>(acc, b, a, la.r, LA::part(pa, w), voff);
+        else mfma_load<IN, 1024 * (Q - (WA ? LA::L : 0))>(acc, b, a, lb.r, LB::part(pb, w), voff);
+    }
+    template <int Q>
     __device__ __forceinline__ void load1(const LA &la, const LB &lb, uint8_t *pa, uint8_t *pb, int w) const
     {
-        if constexpr (WA && Q < LA::L) la.template load<Q>(pa, w);
-        else lb.template load<Q - (WA ? LA::L : 0)>(pb, w);
+        if constexpr (Q < LA::L) lds_load16(la.r, LA::part(pa, w) + 1024 * Q, la.template offset<Q>());
+        else lds_load16(lb.r, LB::part(pb, w) + 1024 * (Q - LA::L), lb.template offset<Q - LA::L>());
     }
-    template <bool WA, int Q>
-    __device__ __forceinline__ uint32_t prepare1(const LA &la, const LB &lb, uint8_t *pa, uint8_t *pb, int w) const
+    // The load, of L in a step, that MFMA m carries (-1: none): spread evenly,
+    // with the first MFMA left free where there are two or more for each.
+    static constexpr int load_of(int m, int l)
     {
-        if constexpr (WA && Q < LA::L) return la.template prepare<Q>(pa, w);
-        else return lb.template prepare<Q - (WA ? LA::L : 0)>(pb, w);
-    }
-    template <bool WA, int Q>
-    __device__ __forceinline__ void issue1(const LA &la, const LB &lb, uint32_t voff) const
-    {
-        if constexpr (WA && Q < LA::L) la.issue(voff);
-        else lb.issue(voff);
+        if (l == 0) return -1;
+        if (kM >= 2 * l) return m % (kM / l) == 1 && m / (kM / l) < l ? m / (kM / l) : -1;
+        return l * (m + 1) / kM > l * m / kM ? l * m / kM : -1;
     }
 
     // One step: MFMAs on cur, fragments of the next step (of panels ra_, rb_)
     // into nxt, and loads into the panels pa and pb.  An MFMA of 16 cycles
     // covers about three other instructions, so reads and loads are dealt out
-    // one by one, and a load's address part goes one MFMA ahead of it.
+    // one by one, and a load's offset is formed one MFMA ahead of it.
     template <bool ODD, class Seek>
     __device__ __forceinline__ void step(f32x4 (&acc)[2 * MI][2 * NB], Frag<MI, NB> &cur, Frag<MI, NB> &nxt, LA &la, LB &lb,
                                          const uint8_t *ra_, const uint8_t *rb_, uint8_t *pa, uint8_t *pb, int w, Seek &&seek)
@@ -255,23 +268,19 @@ struct Tile {
             seek();                  // aim at the pair that this step and the next one load
         }
         __builtin_amdgcn_sched_barrier(0);
+        static_assert(L <= kM, "at most one load an MFMA");
         uint32_t voff = 0;
+        if constexpr (load_of(0, L) == 0) voff = offset1<WA, 0>(la, lb);
         static_for<kM>([&](auto mm) {
             // columns back and forth, so that neighbours share an operand (0.5%)
             constexpr int m = decltype(mm)::value, i = m / (2 * NB), c = m % (2 * NB), j = i % 2 ? 2 * NB - 1 - c : c;
-            mfma_into<IN>(acc[i][j], cur.b[j], cur.a[i]);
+            constexpr int q = load_of(m, L), next = m + 1 < kM ? load_of(m + 1, L) : -1;
+            if constexpr (q >= 0) mfma_load1<WA, q>(acc[i][j], cur.b[j], cur.a[i], la, lb, pa, pb, w, voff);
+            else mfma_into<IN>(acc[i][j], cur.b[j], cur.a[i]);
+            if constexpr (next >= 0) voff = offset1<WA, next>(la, lb);
             if constexpr (m < kRSpan) {
                 static_for<(kR * (m + 1)) / kRSpan - (kR * m) / kRSpan>([&](auto rr) {
                     read1<ODD ? 0 : 1, (kR * m) / kRSpan + decltype(rr)::value>(nxt, ra_, rb_);
-                });
-            }
-            if constexpr (L > 0 && kM >= 2 * L) {
-                constexpr int P = kM / (L > 0 ? L : 1), q = m / P;
-                if constexpr (q < L && m % P == 0) voff = prepare1<WA, q>(la, lb, pa, pb, w);
-                if constexpr (q < L && m % P == 1) issue1<WA, q>(la, lb, voff);
-            } else {
-                static_for<(L * (m + 1)) / kM - (L * m) / kM>([&](auto ll) {
-                    load1<WA, (L * m) / kM + decltype(ll)::value>(la, lb, pa, pb, w);
                 });
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -295,7 +304,7 @@ struct Tile {
 #pragma unroll
         for (int s = 0; s < NA; ++s) {
             seek(s);
-            static_for<LA::L + LB::L>([&](auto q) { load1<true, decltype(q)::value>(la, lb, ring + s * kA, ringb + s * kB, w); });
+            static_for<LA::L + LB::L>([&](auto q) { load1<decltype(q)::value>(la, lb, ring + s * kA, ringb + s * kB, w); });
         }
         s_wait_vm<(NA - 1) * (LA::L + LB::L)>();
         __builtin_amdgcn_s_barrier();
