@@ -78,3 +78,55 @@ def m0_faults(body):
             if before[0] not in (("s_mov_b32", ["m0"]), ("s_add_u32", ["m0"])) or not (before[-1] == ("s_nop", ["0"]) or before[-1][0].startswith("v_mfma")):
                 bad.append((i, before, op))
     return bad
+
+
+# A vector instruction's result is there for an MFMA after 2 wait states, and
+# an MFMA's for anything but the MFMA that adds to the same registers after 18
+# (the longest ones; those of 16 x 16 take fewer).  A scalar register that a
+# vector instruction wrote is there for a memory instruction after 5.
+VALU_TO_MFMA, MFMA_TO_OTHERS, VALU_SGPR_TO_MEMORY = 2, 18, 5
+
+
+def _all(args):
+    return set().union(*map(registers, args)) if args else set()
+
+
+def mfma_faults(body):
+    """MFMAs too soon behind a vector instruction that writes an operand, and
+    instructions that touch an MFMA's result too soon."""
+    bad, now, written, results = [], 0, {}, {}
+    for i, (op, args) in enumerate(body):
+        if op.startswith("v_mfma"):
+            for r in _all(args[1:4]):
+                if now - written.get(r, -100) < VALU_TO_MFMA:
+                    bad.append((i, op, r))
+            # the exact accumulator may follow itself; another overlap may not
+            for r in _all(args[1:4]) & results.keys():
+                t, whole = results[r]
+                if now - t < MFMA_TO_OTHERS and not (r in registers(args[3]) and whole == args[3] == args[0]):
+                    bad.append((i, op, r))
+            now += 1
+            results.update(dict.fromkeys(registers(args[0]), (now, args[0])))
+            continue
+        for r in _all(args) & results.keys():
+            if now - results[r][0] < MFMA_TO_OTHERS:
+                bad.append((i, op, r))
+        now += states(op, args)
+        if op.startswith("v_") and args:
+            written.update(dict.fromkeys(registers(args[0]), now))
+    return bad
+
+
+def sgpr_faults(body):
+    """Buffer instructions too soon behind a vector instruction that writes
+    one of their scalar registers."""
+    bad, now, written = [], 0, {}
+    for i, (op, args) in enumerate(body):
+        if op.startswith("buffer_"):
+            for r in _all(args):
+                if now - written.get(r, -100) < VALU_SGPR_TO_MEMORY:
+                    bad.append((i, op, r))
+        now += states(op, args)
+        if op.startswith("v_") and args:
+            written.update(dict.fromkeys([r for r in registers(args[0]) if r[0] == "s"], now))
+    return bad
