@@ -80,6 +80,8 @@ def lib():
             fn.restype = i32
         L.bsg_workspace_bytes.restype = i64
         L.bsg_workspace_bytes.argtypes = [i32, i64, i64, i64]
+        L.bsg_plan_string.restype = ctypes.c_char_p
+        L.bsg_plan_string.argtypes = [i32, i64, i64, i64]
         L.bsg_status_string.restype = ctypes.c_char_p
         L.bsg_status_string.argtypes = [i32]
         L.bsg_last_error.restype = ctypes.c_char_p
@@ -98,7 +100,8 @@ def symbols():
             "bsg_validate_grouped_gemm_dswiglu",
             "bsg_validate_grouped_gemm_discrete", "bsg_validate_grouped_gemm_srelu_discrete",
             "bsg_check_padded_offsets", "bsg_status_string", "bsg_last_error", "bsg_version",
-            *_FFN_OPS, *("bsg_validate_" + n for n in _FFN_OPS), "bsg_workspace_bytes"]
+            *_FFN_OPS, *("bsg_validate_" + n for n in _FFN_OPS), "bsg_workspace_bytes",
+            "bsg_plan_string"]
 
 
 def _ptr(t):
@@ -438,6 +441,17 @@ def workspace_bytes(name, m, n, k) -> int:
     if b < 0:
         raise BsgError(2, f"{name}: sizes {(m, n, k)} are not sizes")
     return b
+
+
+def plan_string(name, m, n, k) -> str:
+    """How operator `name` goes out at these sizes (see include/bsg.h): for
+    tests and tuning."""
+    if name not in _WS_OPS:
+        raise ValueError(f"no operator named {name!r}")
+    s = lib().bsg_plan_string(_WS_OPS[name], m, n, k)
+    if s is None:
+        raise BsgError(2, lib().bsg_last_error().decode())
+    return s.decode()
 
 
 _TORCH_OF = {F32: torch.float32, F16: torch.float16, BF16: torch.bfloat16}

@@ -13,6 +13,7 @@
 
 #include "../../include/bsg.h"
 #include "ffn/ffn.hpp"
+#include "ffn/plan.hpp"
 #include "launch.hpp"
 
 namespace {
@@ -634,6 +635,39 @@ int64_t bsg_workspace_bytes(int op, int64_t m, int64_t n, int64_t k)
     case BSG_OP_GEMM_GLU_BWD: return bsg::ffn::workspace_gemm_glu_bwd(m, n, k);
     default: return -1;
     }
+}
+
+const char *bsg_plan_string(int op, int64_t m, int64_t n, int64_t k)
+{
+    using namespace bsg::ffn;
+    static thread_local char text[64];
+    if (check_ffn_sizes(m, n, k)) return nullptr;
+    struct Name {
+        char s[24];
+        explicit Name(const Plan &p)
+        {
+            static const char *const shape[4] = {"Big", "Mid", "Small", "Shared"};
+            if (p.splits > 1) snprintf(s, sizeof s, "%s / %d", shape[p.shape], p.splits);
+            else snprintf(s, sizeof s, "%s", shape[p.shape]);
+        }
+    };
+    if (op == BSG_OP_GEMM_I8 || op == BSG_OP_GEMM_GLU || op == BSG_OP_GEMM_GLU_I8) {
+        if (!m || !n) return "none";
+        const Form f = op == BSG_OP_GEMM_I8 ? form_gemm_i8(m, n, k) : form_gemm_glu(m, n, k, op == BSG_OP_GEMM_GLU_I8);
+        if (f.few) snprintf(text, sizeof text, "few %d", f.few);
+        else snprintf(text, sizeof text, "%s", Name(f.tiles).s);
+    } else if (op == BSG_OP_GEMM_GLU_BWD) {
+        const PlanPair p = pair_glu_bwd(m, n, k);
+        const bool x = m && k, w = n && k;
+        if (x && w && p.together) snprintf(text, sizeof text, "dX + dW: %s", Name(p.x).s);
+        else if (x && w) snprintf(text, sizeof text, "dX: %s, dW: %s", Name(p.x).s, Name(p.w).s);
+        else if (x || w) snprintf(text, sizeof text, "%s: %s", x ? "dX" : "dW", Name(x ? p.x : p.w).s);
+        else return "none";
+    } else {
+        fail(BSG_ERR_SHAPE, "op %d is not a bsg_op", op);
+        return nullptr;
+    }
+    return text;
 }
 
 int bsg_validate_quant_i8(const void *x, int8_t *q, float *scale, int64_t m, int64_t k, int x_dtype)

@@ -159,12 +159,11 @@ void go_few(const I8Args &a, hipStream_t s)
 template <int CT>
 void launch(const I8Args &a, hipStream_t s)
 {
-    if (few_is_cheaper(a.m, a.n, a.k)) {
-        if (a.m <= 16) return go_few<CT, 1, 2>(a, s);
-        if (a.m <= 32) return go_few<CT, 2, 2>(a, s);
-        return go_few<CT, 4, 1>(a, s);
-    }
-    const Plan p = plan_of(a.m, a.n, a.k);
+    const Form f = form_gemm_i8(a.m, a.n, a.k);
+    if (f.few == 16) return go_few<CT, 1, 2>(a, s);
+    if (f.few == 32) return go_few<CT, 2, 2>(a, s);
+    if (f.few == 64) return go_few<CT, 4, 1>(a, s);
+    const Plan &p = f.tiles;
     with_shape(p, [&](auto shape, auto split) {
         k_i8<CT, decltype(shape), decltype(split)::value><<<p.grid(), 256, 0, s>>>(a, p.mt, p.nt, p.splits);
     });
@@ -175,9 +174,8 @@ void launch(const I8Args &a, hipStream_t s)
 
 int64_t workspace_gemm_i8(int64_t m, int64_t n, int64_t k)
 {
-    if (few_is_cheaper(m, n, k)) return 0;
-    const Plan p = plan_of(m, n, k);
-    return p.splits > 1 ? 4 * m * n * p.splits : 0;
+    const Form f = form_gemm_i8(m, n, k);
+    return !f.few && f.tiles.splits > 1 ? 4 * m * n * f.tiles.splits : 0;
 }
 
 hipError_t launch_gemm_i8(const I8Args &a, hipStream_t s)

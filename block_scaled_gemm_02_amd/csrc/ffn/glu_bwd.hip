@@ -179,10 +179,6 @@ __global__ __launch_bounds__(256) void k_join(const float *sums, void *out0, voi
     else store4<DT>(out1, 4 * (i - first4), s);
 }
 
-PlanPair plans(int64_t m, int64_t n, int64_t k)
-{
-    return plan_pair(m, k, 2 * ((2 * n + 127) / 128 * 128), 2 * n, k, 2 * m);
-}
 int64_t d_bytes(int64_t m, int64_t n) { return (4 * m * n + 255) / 256 * 256; }
 
 }  // namespace
@@ -190,7 +186,7 @@ int64_t d_bytes(int64_t m, int64_t n) { return (4 * m * n + 255) / 256 * 256; }
 int64_t workspace_gemm_glu_bwd(int64_t m, int64_t n, int64_t k)
 {
     // dX and the weight gradients follow each other: their splits share the space
-    const auto [x, w, together] = plans(m, n, k);
+    const auto [x, w, together] = pair_glu_bwd(m, n, k);
     const int64_t sx = x.splits > 1 ? 4 * m * k * x.splits : 0, sw = w.splits > 1 ? 8 * n * k * w.splits : 0;
     return d_bytes(m, n) + (sx > sw ? sx : sw);
 }
@@ -208,7 +204,7 @@ hipError_t launch_gemm_glu_bwd(const GluBwdArgs &a, hipStream_t s)
                     (const uint4 *)a.dh, (const uint4 *)a.g, (const uint4 *)a.u, (uint4 *)d, count, (uint32_t)(a.n / 8));
             });
         }
-        const auto [px, pw, together] = plans(a.m, a.n, a.k);
+        const auto [px, pw, together] = pair_glu_bwd(a.m, a.n, a.k);
         const bool x = a.dx && a.m && a.k, w = a.dw_gate && a.n && a.k;
         if (x && w && together) {
             with_shape(px, [&, &px = px, &pw = pw](auto shape, auto) {

@@ -189,12 +189,11 @@ void launch(const GluArgs &a, hipStream_t s)
 {
     with_act(a.act, [&](auto act) {
         constexpr int A = decltype(act)::value;
-        if (few_is_cheaper(a.m, 2 * a.n, a.k * in_bytes(IN))) {
-            if (a.m <= 16) return go_few<IN, DT, A, SAVE, 1, 2>(a, s);
-            if (a.m <= 32) return go_few<IN, DT, A, SAVE, 2, 2>(a, s);
-            return go_few<IN, DT, A, SAVE, 4, 1>(a, s);
-        }
-        const Plan p = plan_of(a.m, 2 * a.n, a.k * in_bytes(IN));
+        const Form f = form_gemm_glu(a.m, a.n, a.k, IN == IN_I8);
+        if (f.few == 16) return go_few<IN, DT, A, SAVE, 1, 2>(a, s);
+        if (f.few == 32) return go_few<IN, DT, A, SAVE, 2, 2>(a, s);
+        if (f.few == 64) return go_few<IN, DT, A, SAVE, 4, 1>(a, s);
+        const Plan &p = f.tiles;
         with_shape(p, [&](auto shape, auto split) {
             k_glu<IN, DT, A, SAVE, decltype(shape), decltype(split)::value><<<p.grid(), 256, 0, s>>>(a, p.mt, p.nt, p.splits);
         });
@@ -206,9 +205,8 @@ void launch(const GluArgs &a, hipStream_t s)
 
 int64_t workspace_gemm_glu(int64_t m, int64_t n, int64_t k, bool in_i8)
 {
-    if (few_is_cheaper(m, 2 * n, in_i8 ? k : 2 * k)) return 0;
-    const Plan p = plan_of(m, 2 * n, in_i8 ? k : 2 * k);
-    return p.splits > 1 ? 8 * m * n * p.splits : 0;
+    const Form f = form_gemm_glu(m, n, k, in_i8);
+    return !f.few && f.tiles.splits > 1 ? 8 * m * n * f.tiles.splits : 0;
 }
 
 hipError_t launch_gemm_glu(const GluArgs &a, hipStream_t s)

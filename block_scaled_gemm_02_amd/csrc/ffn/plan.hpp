@@ -116,13 +116,34 @@ inline PlanPair plan_pair(int64_t xr, int64_t xc, int64_t xk, int64_t wr, int64_
 // / 11.8; int8 7168 x 2048, 24 tokens 7.2 / 8.0, 40 9.7 / 8.1; gated bf16 2048 x
 // 7168, 16 tokens 15.4 / 17.4, 24 18.7 / 17.5; gated bf16 8192 x 4096, 8 tokens
 // 28.7 / 33.5, 16 35.6 / 35.3; gated bf16 512 x 512, 64 tokens 4.6 / 5.1.
-inline bool few_is_cheaper(int64_t tokens, int64_t cols, int64_t kbytes)
+inline double few_us(int64_t tokens, int64_t cols, int64_t kbytes)
 {
-    if (tokens > 64) return false;
     const double rounds = (double)((cols + 4095) / 4096);
-    const double t = (tokens > 32 ? 3.8 : 2.5) + (double)cols * (double)kbytes / 5.2e6 +
-                     rounds * (double)std::max<int64_t>(0, tokens - 6) * (double)kbytes / 45000.0;
-    return t <= plan_of(tokens, cols, kbytes).us;
+    return (tokens > 32 ? 3.8 : 2.5) + (double)cols * (double)kbytes / 5.2e6 +
+           rounds * (double)std::max<int64_t>(0, tokens - 6) * (double)kbytes / 45000.0;
+}
+
+// How a product goes out: in the few-token kernel's form for up to 16, 32 or
+// 64 tokens, or (few = 0) in tiles.
+struct Form {
+    int few;
+    Plan tiles;
+};
+inline Form form_of(int64_t tokens, int64_t cols, int64_t kbytes)
+{
+    const Plan p = plan_of(tokens, cols, kbytes);
+    if (tokens > 64 || few_us(tokens, cols, kbytes) > p.us) return {0, p};
+    return {tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64, p};
+}
+
+// The operators' products: their launches, workspace sizes and plan strings
+// all come from these.
+inline Form form_gemm_i8(int64_t m, int64_t n, int64_t k) { return form_of(m, n, k); }
+inline Form form_gemm_glu(int64_t m, int64_t n, int64_t k, bool in_i8) { return form_of(m, 2 * n, in_i8 ? k : 2 * k); }
+// x: dX, whose K is two ranges of n, each padded to whole pairs; w: both weight gradients
+inline PlanPair pair_glu_bwd(int64_t m, int64_t n, int64_t k)
+{
+    return plan_pair(m, k, 2 * ((2 * n + 127) / 128 * 128), 2 * n, k, 2 * m);
 }
 
 }  // namespace ffn

@@ -407,6 +407,14 @@ typedef enum bsg_op {
  * type and option); -1 for an unknown op or a negative size. */
 int64_t bsg_workspace_bytes(int op, int64_t m, int64_t n, int64_t k);
 
+/* How the operator's products go out at these sizes, as a text: "few T" (the
+ * kernel for up to T tokens), or the tile's shape, with " / P" where K is in P
+ * parts; for gemm_glu_bwd that of dX and of the weight gradients, or of both
+ * where they are one launch.  NULL for an unknown op or sizes that are refused.
+ * Valid until the thread's next call.  For tests and tuning: the texts are no
+ * part of the interface. */
+const char *bsg_plan_string(int op, int64_t m, int64_t n, int64_t k);
+
 /*
  * quant_i8 -- rows to symmetric 8-bit integers, one scale a row:
  *     t = max(max_k |x[m,k]|, 2^-100)
