@@ -21,3 +21,7 @@ BACKWARD = {
     "dX: Mid / P, dW: Small": (1, 968, 72), "dX: Mid / P, dW: Mid": (387, 8656, 16), "dX: Mid, dW: Big": (985, 2160, 3728),
     "dX: Shared, dW: Mid / P": (11229, 8, 264), "dX: Small, dW: Mid / P": (2013, 8, 72),
     "dX: Big, dW: Mid / P": (9819, 136, 1376)}
+
+# (m, n, k) of a block whose products have K in parts: the forward ones, the
+# down projection from integers and dX, the weight gradients
+PARTS = [(100, 272, 9008), (100, 4512, 272), (9000, 144, 272)]

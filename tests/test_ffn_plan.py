@@ -63,3 +63,11 @@ def test_plan_string():
     with pytest.raises(bsg.BsgError):
         bsg.plan_string("gemm_i8", -1, 8, 8)
     assert bsg.lib().bsg_plan_string(9, 1, 1, 1) is None
+
+
+def test_sizes_with_k_in_parts():
+    """What the GPU test of repeats, streams and graphs relies on."""
+    (a, b, c) = F.PARTS
+    assert form("gemm_glu", a) == form("gemm_glu_i8", a) == "Mid / P"
+    assert form("gemm_i8", (b[0], b[2], b[1])) == "Mid / P" and form("gemm_glu_bwd", b).startswith("dX: Mid / P")
+    assert form("gemm_glu_bwd", c).endswith("dW: Mid / P")

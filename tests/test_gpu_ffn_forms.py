@@ -143,3 +143,81 @@ def test_gemm_glu_bwd(name, dt):
     dg, du = dh.double() * uu.double() * on, dh.double() * gg.double() * on
     assert torch.equal(dx, (dg @ wg.double() + du @ wu.double()).to(dt))
     assert torch.equal(dwg, (dg.t() @ x.double()).to(dt)) and torch.equal(dwu, (du.t() @ x.double()).to(dt))
+
+
+class Block:
+    """A block's training pass and serving pass, each output and workspace
+    between sentinels."""
+
+    def __init__(self, m, n, k):
+        g = gen(m + n + k)
+        self.size = m, n, k
+        self.x, self.dh = rnd(g, m, k, dt=BF), rnd(g, m, n, dt=BF)
+        self.wg, self.wu = rnd(g, n, k, dt=BF, std=k ** -0.5), rnd(g, n, k, dt=BF, std=k ** -0.5)
+        self.qg, self.qu, self.qd = ints(g, n, k), ints(g, n, k), ints(g, k, n)
+        self.sn, self.sk = torch.full((n,), 1e-2 * k ** -0.5, device=DEV), torch.full((k,), 1e-2, device=DEV)
+        i8 = torch.int8
+        self.out = {name: Guarded(s, dt) for name, (s, dt) in dict(
+            h=((m, n), BF), g=((m, n), BF), u=((m, n), BF), dx=((m, k), BF), dwg=((n, k), BF), dwu=((n, k), BF),
+            q=((m, k), i8), s=((m,), F32), h8=((m, n), BF), qh=((m, n), i8), sh=((m,), F32), y=((m, k), BF)).items()}
+        self.ws = {op: Guarded((bsg.workspace_bytes(op, m, *((k, n) if op == "gemm_i8" else (n, k))),), torch.uint8, 255)
+                   for op in ("gemm_glu", "gemm_glu_bwd", "gemm_glu_i8", "gemm_i8")}
+
+    def __call__(self):
+        (m, n, k), o, w = self.size, {a: b.t for a, b in self.out.items()}, {a: b.t for a, b in self.ws.items()}
+        bsg.gemm_glu(self.x, self.wg, self.wu, o["h"], o["g"], o["u"], m, n, k, workspace=w["gemm_glu"])
+        bsg.gemm_glu_bwd(self.dh, self.x, self.wg, self.wu, o["g"], o["u"], o["dx"], o["dwg"], o["dwu"], m, n, k,
+                         workspace=w["gemm_glu_bwd"])
+        bsg.quant_i8(self.x, o["q"], o["s"], m, k)
+        bsg.gemm_glu_i8(o["q"], self.qg, self.qu, o["s"], self.sn, self.sn, o["h8"], m, n, k, workspace=w["gemm_glu_i8"])
+        bsg.quant_i8(o["h8"], o["qh"], o["sh"], m, n)
+        bsg.gemm_i8(o["qh"], self.qd, o["sh"], self.sk, None, o["y"], m, k, n, workspace=w["gemm_i8"])
+
+    def same(self, ref, what):
+        for name, o in self.out.items():
+            o.check()
+            assert torch.equal(o.t.view(torch.uint8), ref.out[name].t.view(torch.uint8)), (what, name)
+        for w in self.ws.values():
+            w.check()
+
+
+@pytest.mark.parametrize("size", F.PARTS)
+def test_parts_of_k_repeated_on_streams_and_in_a_graph(size):
+    """The tiles' partial sums and the kernels that join them: calls one after
+    another on one workspace, on two streams at once (a workspace each), and
+    replays of a graph between eager work give the first call's bits."""
+    say("parts of K", size)
+    ref = Block(*size)
+    ref()
+    torch.cuda.synchronize()
+    again = Block(*size)
+    for _ in range(3):
+        again()
+    torch.cuda.synchronize()
+    again.same(ref, "in a row")
+    runs = [(Block(*size), torch.cuda.Stream()) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(2):
+        for b, st in runs:
+            with torch.cuda.stream(st):
+                b()
+    torch.cuda.synchronize()
+    for b, _ in runs:
+        b.same(ref, "streams")
+    b, side = Block(*size), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        b()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b()
+    torch.cuda.synchronize()
+    for r in range(3):
+        for o in b.out.values():
+            o.t.fill_(3)
+        graph.replay()
+        again()
+        torch.cuda.synchronize()
+        b.same(ref, f"replay {r}")
+        again.same(ref, f"beside replay {r}")
