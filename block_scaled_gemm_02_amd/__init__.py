@@ -561,7 +561,8 @@ def gemm_glu_i8(a, w_gate, w_up, a_scale, gate_scale, up_scale, h, m, n, k, act=
 def gemm_glu_bwd(dh, x, w_gate, w_up, g, u, dx, dw_gate, dw_up, m, n, k, act="silu", dtype=None,
                  workspace=None, stream=None, validate_only=False):
     """Gradients of gemm_glu from dh and the saved g and u (see include/bsg.h).
-    dx, or dw_gate and dw_up together, may be None."""
+    dx, or dw_gate and dw_up together, may be None.  In fp16 dG and dU have
+    that type's range, so the loss is scaled as for any fp16 gradient."""
     dt = _code(dtype, dh)
     mn, mk, nk = _out_bytes(dt, m * n), _out_bytes(dt, m * k), _out_bytes(dt, n * k)
     td = _TORCH_OF.get(dt)

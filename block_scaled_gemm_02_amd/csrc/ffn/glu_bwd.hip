@@ -19,7 +19,11 @@ namespace ffn {
 namespace {
 
 // dG and dU are rounded to 16 bits here, the type that the matrix cores read;
-// G, U and dH are of that type themselves.
+// G, U and dH are of that type themselves.  It adds one rounding to the
+// output's: the gradients are off by 1.41 times what rounding the exact ones
+// gives (bf16 0.0023 of their norm for 0.0017, fp16 0.00029 for 0.00021).
+// Keeping fp32 would take two 16-bit parts each and twice the MFMAs.  In fp16
+// it also bounds their range (65504, 2^-25), which scaling dH moves.
 template <int DT, int ACT>
 __global__ __launch_bounds__(256) void k_dact(const uint4 *dh, const uint4 *g, const uint4 *u, uint4 *d, int64_t count,
                                               uint32_t n8)

@@ -467,6 +467,12 @@ int gemm_glu_i8(const int8_t *a, const int8_t *w_gate, const int8_t *w_up, const
  *     dX = dG Wg + dU Wu            dWg = dG^T X       dWu = dU^T X
  *   All tensors fp16 or all bf16.  dG and dU are formed in fp32 and rounded
  *   once to that type, which the matrix cores read.  act'(0) of ReLU is 0.
+ *   In fp16 that bounds them: |dG| or |dU| past 65504 is infinity, and the
+ *   gradients it enters are not finite, although their own sums might be; below
+ *   2^-25 it is 0, and from there to 2^-14 it has fewer digits.  Gradients are
+ *   linear in dH, so a power of two on dH moves both ends, and comes off the
+ *   outputs exactly: scale the loss, and lower the scale where an output is
+ *   not finite.  bf16 has fp32's range.
  *   dx may be NULL (no input gradient), and so may dw_gate and dw_up together
  *   (frozen weights; x may then be NULL too).  Outputs are overwritten, and
  *   are the same from call to call: no sum depends on the order of arrival.
