@@ -380,7 +380,11 @@ int bsg_check_padded_offsets(const int32_t *padded_offsets, int64_t num_experts,
  * Feed-forward operators: what a gated feed-forward block runs in training
  * (16-bit operands) and in serving (8-bit integers with scales).  All tensors
  * are dense and row-major; weights are (out, in), as for the other entry
- * points.  M counts tokens and takes any value >= 0; rows are whole 16-byte
+ * points.  Infinities and NaN go through as the formulas have them in floating
+ * point, and spoil only the rows and columns that they enter.  act of -infinity
+ * is NaN for SiLU and GELU (-infinity times 0) and 0 for ReLU; act' of either
+ * infinity is NaN for SiLU and GELU.
+ * M counts tokens and takes any value >= 0; rows are whole 16-byte
  * pieces (ALIGN otherwise), so N and K are multiples of 8 (16-bit), K of 16
  * (integers), N of 4 (fp32 C).  K = 0 is an empty sum.  Sums are held in fp32
  * (16-bit operands) or int32 (integers, exact).  Sizes past 2^22 tokens, 2^20
