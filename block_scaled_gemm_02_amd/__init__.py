@@ -439,8 +439,12 @@ def workspace_bytes(name, m, n, k) -> int:
         raise ValueError(f"no operator named {name!r}")
     b = lib().bsg_workspace_bytes(_WS_OPS[name], m, n, k)
     if b < 0:
-        raise BsgError(2, f"{name}: sizes {(m, n, k)} are not sizes")
+        _refuse_sizes(m, n, k)
     return b
+
+
+def _refuse_sizes(*sizes):
+    raise BsgError(2 if min(sizes) < 0 else 5, lib().bsg_last_error().decode())
 
 
 def plan_string(name, m, n, k) -> str:
@@ -450,7 +454,7 @@ def plan_string(name, m, n, k) -> str:
         raise ValueError(f"no operator named {name!r}")
     s = lib().bsg_plan_string(_WS_OPS[name], m, n, k)
     if s is None:
-        raise BsgError(2, lib().bsg_last_error().decode())
+        _refuse_sizes(m, n, k)
     return s.decode()
 
 

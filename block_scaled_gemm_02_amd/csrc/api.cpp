@@ -627,13 +627,13 @@ static bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3
 
 int64_t bsg_workspace_bytes(int op, int64_t m, int64_t n, int64_t k)
 {
-    if (m < 0 || n < 0 || k < 0) return -1;
+    if (check_ffn_sizes(m, n, k)) return -1;
     switch (op) {
     case BSG_OP_GEMM_I8: return bsg::ffn::workspace_gemm_i8(m, n, k);
     case BSG_OP_GEMM_GLU: return bsg::ffn::workspace_gemm_glu(m, n, k, false);
     case BSG_OP_GEMM_GLU_I8: return bsg::ffn::workspace_gemm_glu(m, n, k, true);
     case BSG_OP_GEMM_GLU_BWD: return bsg::ffn::workspace_gemm_glu_bwd(m, n, k);
-    default: return -1;
+    default: fail(BSG_ERR_SHAPE, "op %d is not a bsg_op", op); return -1;
     }
 }
 

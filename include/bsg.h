@@ -408,7 +408,7 @@ typedef enum bsg_op {
 } bsg_op;
 
 /* Scratch bytes that the operator takes at these sizes (enough for every
- * type and option); -1 for an unknown op or a negative size. */
+ * type and option); -1 for an unknown op or sizes that are refused. */
 int64_t bsg_workspace_bytes(int op, int64_t m, int64_t n, int64_t k);
 
 /* How the operator's products go out at these sizes, as a text: "few T" (the

@@ -71,3 +71,17 @@ def test_sizes_with_k_in_parts():
     assert form("gemm_glu", a) == form("gemm_glu_i8", a) == "Mid / P"
     assert form("gemm_i8", (b[0], b[2], b[1])) == "Mid / P" and form("gemm_glu_bwd", b).startswith("dX: Mid / P")
     assert form("gemm_glu_bwd", c).endswith("dW: Mid / P")
+
+
+@pytest.mark.parametrize("size", [((1 << 22) + 1, 8, 16), (8, (1 << 20) + 8, 16), (8, 8, (1 << 20) + 16), (1 << 40, 1 << 30, 8),
+                                  (1 << 31, 1 << 30, 8), ((1 << 63) - 1, 8, 16)])
+def test_sizes_that_calls_refuse_have_no_workspace(size):
+    """Past the limits on sizes the bytes would wrap around: to 0 at the
+    fourth of these."""
+    for op in (*F.PRODUCTS, "gemm_glu_bwd"):
+        with pytest.raises(bsg.BsgError) as err:
+            bsg.workspace_bytes(op, *size)
+        assert err.value.status == 5
+        with pytest.raises(bsg.BsgError) as err:
+            bsg.plan_string(op, *size)
+        assert err.value.status == 5
