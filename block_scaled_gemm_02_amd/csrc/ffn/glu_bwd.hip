@@ -5,6 +5,11 @@
 // it with the weights as they lie (their K rows are n); both weight gradients
 // are one product of 2n rows contracted over the tokens.  The two products do
 // not depend on each other and go out as one launch where that is cheaper.
+// One of them alone keeps its part of that choice, so that its bits do not
+// depend on the other; chosen for itself it would be faster (bf16, us, dX alone
+// / dWg and dWu alone, in brackets chosen for themselves): 1003 x 1408 x 2048
+// 29.9 (24.5) / 24.2 (24.0), 200 x 4528 x 2904 56.5 (30.2, K in parts) / 40.0
+// (33.5), 4096 x 1408 x 2048 64.5 (53.2) / 84.1 (62.9).
 //
 // bf16 8192 x 8192 x 4096: the pass 105 us, 6.3 TB/s (writing dG and dU, and
 // reading them back, is what keeps the products plain: formed inside dX they

@@ -480,6 +480,9 @@ int gemm_glu_i8(const int8_t *a, const int8_t *w_gate, const int8_t *w_up, const
  *   dx may be NULL (no input gradient), and so may dw_gate and dw_up together
  *   (frozen weights; x may then be NULL too).  Outputs are overwritten, and
  *   are the same from call to call: no sum depends on the order of arrival.
+ *   Either half alone has the bits that it has beside the other.  It goes out
+ *   in the form chosen for both, which costs up to twice the time of one chosen
+ *   for it alone.
  */
 int gemm_glu_bwd(const void *dh, const void *x, const void *w_gate, const void *w_up,
                  const void *g, const void *u, void *dx, void *dw_gate, void *dw_up,
