@@ -10,10 +10,12 @@
 // Weights are the MFMA's first operand: register v of lane (t, g) is channel
 // 4g + v of token t.
 //
-// Bound by HBM and, when small, by its launch (about 2.5 us): gated bf16 1 x
-// 2048 x 7168 (58.7 MB) 10.6 us, 5.5 TB/s (a large copy reaches 4.9); gated
-// int8 8 x 2048 x 7168 (29.5 MB) 7.7 us; int8 1 x 7168 x 2048 (14.7 MB) 4.9
-// us.  (The order in which workgroups walk K made no difference.)
+// Bound by HBM and, when small, by its launch (about 2.5 us).  Sets of weights
+// in turn that no cache holds (640 MB of them) / that the 256 MB memory-side
+// cache does: gated bf16 1 x 2048 x 7168 (58.7 MB) 12.5 us, 4.7 TB/s / 10.7; 1 x
+// 8192 x 4096 (134 MB) 26.9 us, 5.0 TB/s (a large copy reaches 4.9); gated int8
+// 8 x 2048 x 7168 (29.5 MB) 8.4 us / 7.6; int8 1 x 7168 x 2048 (14.7 MB) 5.2 us
+// / 4.9.  (The order in which workgroups walk K made no difference.)
 #pragma once
 #include "tile.hpp"
 

@@ -2,9 +2,10 @@
 //
 // int32 sums; each is converted to fp32, which rounds it to 24 bits, only to
 // meet its scales, and C is rounded once more to its type.  8192^3 runs in
-// 379-389 us, 2830-2900 TOPS, the matrix cores 75% busy at the clock that the
+// 374-384 us, 2860-2940 TOPS, the matrix cores 76% busy at the clock that the
 // power limit leaves (on zeros 280 us); 67 x 4096, K 7168 in 4 parts in 13.2
-// us, 11.2 of them the tiles, whose loads into LDS bound them.
+// us, and in 16.9 from weights that no cache holds, 14 of them the tiles, on
+// half of the compute units.
 #include "few.hpp"
 
 namespace bsg {

@@ -13,10 +13,10 @@
 //
 // bf16 8192 x 8192 x 4096: the pass 105 us, 6.3 TB/s (writing dG and dU, and
 // reading them back, is what keeps the products plain: formed inside dX they
-// would be computed again for every tile of columns); the products 1.47-1.53
-// ms, 1440-1490 TFLOP/s, 78% MFMA busy at the power limit.  fp16 1003 x 1408 x
-// 2048: 33 us, 4 of them the pass, and the products (Shared tiles) bound by
-// their loads into LDS.
+// would be computed again for every tile of columns); the products 1.47-1.51
+// ms, 1450-1500 TFLOP/s, 76% MFMA busy at the power limit.  fp16 1003 x 1408 x
+// 2048: 32 us, 4 of them the pass, and the products (Shared tiles) waiting for
+// their loads into LDS; 39 us from operands that no cache holds.
 #include "tile.hpp"
 
 namespace bsg {

@@ -2,11 +2,11 @@
 //
 // G and U stay in fp32 (int32 sums times their scales) up to H, which is
 // rounded once; where they are kept they are rounded by themselves.  bf16 8192
-// x 8192 x 4096 with both kept: 757-792 us, 1390-1450 TFLOP/s, 76% MFMA busy at
-// the power limit (on zeros 535 us); int8 4001 x 8192 x 4096 with gelu: 205-213
+// x 8192 x 4096 with both kept: 748-765 us, 1440-1470 TFLOP/s, 76% MFMA busy at
+// the power limit (on zeros 535 us); int8 4001 x 8192 x 4096 with gelu: 200-210
 // us, of which a quarter are prologues and epilogues of four rounds of tiles;
-// fp16 509 x 2048 x 7168: 39-41 us, bound by the loads into LDS (Small tiles,
-// 20 TB/s over the card).
+// fp16 509 x 2048 x 7168: 39-41 us, waiting for the loads into LDS (Small tiles,
+// 709 MB, 18 TB/s over the card), and 54.8 us from operands that no cache holds.
 #include "few.hpp"
 
 namespace bsg {

@@ -30,7 +30,8 @@ struct Plan {
 //   * the operands come from memory at 4.9 TB/s (and 3.5 us of launch);
 //   * splitting K (few tiles, long K) costs 1.5 us (a second kernel, less the
 //     epilogue) and the partial sums' way to memory and back at 2.2 TB/s of them.
-// Measured (us, Big / Mid / Small / Shared / Mid with K in parts): 67 x 4096, K
+// Measured, with the operands in the memory-side cache (us, Big / Mid / Small /
+// Shared / Mid with K in parts): 67 x 4096, K
 // 7168 int8: 62.1 / 23.6 / 18.4 / - / 13.3 (4 parts); 512 x 4096, K 4096 int8:
 // 39.4 / 16.5 / 13.7 / - / 17.9 (2); 1600 x 2048, K 7168 int8: - / 29.8 / 35.7
 // / 31.9; gated fp16 509 x 2048, K 7168: 114 / 44.9 / 38.9 / - / 43.5 (2); gated
@@ -112,7 +113,8 @@ inline PlanPair plan_pair(int64_t xr, int64_t xc, int64_t xk, int64_t wr, int64_
 // workgroup of 16 weight rows reads from the L2 at 45 bytes a nanosecond and
 // compute unit (the first six hide behind the weights); the form for 33 to 64
 // tokens, with less of the weights in flight, takes 1.3 us more.  Measured, few
-// / tiles (us): int8 4096 x 7168, 16 tokens 8.6 / 11.2, 24 11.0 / 11.3, 40 15.3
+// / tiles (us, the weights in the memory-side cache; from HBM the form that is
+// taken needs 0.5 to 5 us more): int8 4096 x 7168, 16 tokens 8.6 / 11.2, 24 11.0 / 11.3, 40 15.3
 // / 11.8; int8 7168 x 2048, 24 tokens 7.2 / 8.0, 40 9.7 / 8.1; gated bf16 2048 x
 // 7168, 16 tokens 15.4 / 17.4, 24 18.7 / 17.5; gated bf16 8192 x 4096, 8 tokens
 // 28.7 / 33.5, 16 35.6 / 35.3; gated bf16 512 x 512, 64 tokens 4.6 / 5.1.

@@ -4,8 +4,12 @@
 //
 // One pass over the row, which stays in registers between the maximum and
 // the codes (up to 4 groups of 16 elements a thread of 256; the rest of a
-// longer row is read a second time).  Bound by memory: 16384 x 7168 fp16
-// (352 MB) takes 62 us, 5.6 TB/s (a large copy reaches 4.9).
+// longer row is read a second time).  Bound by memory from about 2048 elements
+// a row on: 16384 x 7168 fp16 (352 MB) takes 62 us, 5.6 TB/s (a large copy
+// reaches 4.9), fp32 108 us, 5.5 TB/s; 16384 x 2048 bf16 20.9 us, 4.8 TB/s, fp32
+// 30.3 us, 5.5 TB/s.  Shorter rows are bound by their number, a workgroup
+// each, most of whose threads have nothing to do: 16384 rows of 256 to 1024
+// elements take 12.6-14.1 us in any type, for 5.1 us of memory at 512 of bf16.
 #include "act.hpp"
 
 namespace bsg {

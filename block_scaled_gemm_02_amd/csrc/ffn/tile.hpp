@@ -11,7 +11,7 @@
 // and written twice as often, and at these sizes the card runs at its power
 // limit: on random operands the 16x16 ones are 9% faster (int8 8192^3 418 ->
 // 381 us) and 6% (bf16, gated 8192 x 8192 x 4096, 814 -> 763 us), though on
-// zeros they are 1% slower.
+// zeros they are 1% slower.  (Both now 374-384 and 748-765 us.)
 //
 // The LDS holds a ring of panels, a pair of A or B each, filled by
 // direct-to-LDS loads (buffer_load_dwordx4 ... lds) that no register passes
@@ -361,12 +361,17 @@ __device__ __forceinline__ void store4(void *p, int64_t i, float4 v)
 // loads and epilogue hide behind the other (us, Mid / Shared: int8 2048 x 4096,
 // K 2048 24.3 / 20.5; gated bf16 2000 x 2048, K 4096 64.2 / 57.5; the gradients
 // of 1003 x 1408 x 2048 36.2 / 30.7; but int8 67 x 4096, K 7168 in 4 parts, one
-// workgroup a compute unit, 13.3 / 14.1).  Below Big the
-// loads bound the time, not the matrix cores: a CU's direct-to-LDS loads reach
-// about 50 bytes a cycle, 32 KB (Mid) or 24 KB (Small) a pair for 512 or 256
-// cycles of MFMA.  (Letting the four waves divide a pair's K instead of the
-// tile, so that no fragment is read from LDS twice, gained nothing for that
-// reason and its joining of the four sums cost 2 us.)
+// workgroup a compute unit, 13.3 / 14.1).  Below Big the loads into the LDS set
+// the time, not the matrix cores: 32 KB (Mid) or 24 KB (Small) a pair for 512 or
+// 256 cycles of MFMA.  With all compute units at work that is 18-20 TB/s over
+// the card, 30-40 bytes a cycle for each; with half of them a Mid tile's pair
+// takes 0.36 us for 0.47.  So it is something that the units share, and what
+// has not been found: with K longer by one or two 128-byte lines, which spreads
+// a pair's rows otherwise over the L2s, a product takes the same time a pair.
+// Cold operands come on top of it: gated fp16 509 x 2048 x 7168 (68 MB) 38.9 us
+// from the memory-side cache, 54.8 from HBM.  (Letting the four waves divide a
+// pair's K instead of the tile, so that no fragment is read from LDS twice,
+// gained nothing for that reason and its joining of the four sums cost 2 us.)
 template <int MI_, int NB_, int SA, int SB>
 struct Shape {
     static constexpr int MI = MI_, NB = NB_, TM = 64 * MI, TN = 64 * NB;
