@@ -8,7 +8,9 @@ if libbsg.so is missing or a call fails, a RuntimeError is raised.
 Entry points keep the C names:
     gemm_amax, grouped_gemm, grouped_gemm_srelu, grouped_gemm_dswiglu,
     gemm_proj_rope_mxfp8, grouped_gemm_discrete, grouped_gemm_srelu_discrete,
-    quant_i8, gemm_i8, gemm_glu, gemm_glu_i8, gemm_glu_bwd
+    quant_i8, gemm_i8, gemm_glu, gemm_glu_i8, gemm_glu_bwd,
+    moe_sort, moe_gather, moe_gather_bwd, moe_combine, moe_combine_bwd,
+    quant_fp8, gemm_fp8, grouped_gemm_fp8, grouped_gemm_fp8_wgrad
 and validate_only=True calls the host-only check bsg_validate_<name>.
 """
 from __future__ import annotations
@@ -30,7 +32,10 @@ STATUS = {0: "OK", 1: "NULLPTR", 2: "SHAPE", 3: "DTYPE", 4: "ALIGN", 5: "UNSUPPO
 # the feed-forward operators, bsg_act and bsg_op
 _FFN_OPS = ["quant_i8", "gemm_i8", "gemm_glu", "gemm_glu_i8", "gemm_glu_bwd"]
 _ACTS = {"silu": 0, "gelu_tanh": 1, "relu": 2}
-_WS_OPS = {"gemm_i8": 0, "gemm_glu": 1, "gemm_glu_i8": 2, "gemm_glu_bwd": 3}
+_WS_OPS = {"gemm_i8": 0, "gemm_glu": 1, "gemm_glu_i8": 2, "gemm_glu_bwd": 3, "moe_sort": 4, "gemm_fp8": 5}
+# the expert operators
+_MOE_OPS = ["moe_sort", "moe_gather", "moe_gather_bwd", "moe_combine", "moe_combine_bwd", "quant_fp8", "gemm_fp8",
+            "grouped_gemm_fp8", "grouped_gemm_fp8_wgrad"]
 
 
 class BsgError(RuntimeError):
@@ -71,8 +76,17 @@ def lib():
             "gemm_glu": [p] * 7 + [i64] * 4 + [i32, i32, p],
             "gemm_glu_i8": [p] * 8 + [i64] * 4 + [i32, i32, p],
             "gemm_glu_bwd": [p] * 10 + [i64] * 4 + [i32, i32, p],
+            "moe_sort": [p] * 6 + [i64] * 5 + [p],
+            "moe_gather": [p] * 8 + [i64] * 5 + [i32] * 3 + [p],
+            "moe_gather_bwd": [p] * 5 + [i64] * 4 + [i32, p],
+            "moe_combine": [p] * 4 + [i64] * 4 + [i32, p],
+            "moe_combine_bwd": [p] * 8 + [i64] * 5 + [i32] * 2 + [p],
+            "quant_fp8": [p] * 5 + [i64] * 3 + [i32] * 3 + [p],
+            "gemm_fp8": [p] * 6 + [i64] * 4 + [i32] * 2 + [p],
+            "grouped_gemm_fp8": [p] * 7 + [i64] * 5 + [i32] * 2 + [p],
+            "grouped_gemm_fp8_wgrad": [p] * 6 + [i64] * 4 + [i32] * 2 + [p],
         }
-        for name in _FFN_OPS:
+        for name in _FFN_OPS + _MOE_OPS:
             sigs["bsg_validate_" + name] = sigs[name][:-1]
         for name, args in sigs.items():
             fn = getattr(L, name)
@@ -80,6 +94,8 @@ def lib():
             fn.restype = i32
         L.bsg_workspace_bytes.restype = i64
         L.bsg_workspace_bytes.argtypes = [i32, i64, i64, i64]
+        L.bsg_moe_rows.restype = i64
+        L.bsg_moe_rows.argtypes = [i64] * 3
         L.bsg_plan_string.restype = ctypes.c_char_p
         L.bsg_plan_string.argtypes = [i32, i64, i64, i64]
         L.bsg_status_string.restype = ctypes.c_char_p
@@ -101,7 +117,7 @@ def symbols():
             "bsg_validate_grouped_gemm_discrete", "bsg_validate_grouped_gemm_srelu_discrete",
             "bsg_check_padded_offsets", "bsg_status_string", "bsg_last_error", "bsg_version",
             *_FFN_OPS, *("bsg_validate_" + n for n in _FFN_OPS), "bsg_workspace_bytes",
-            "bsg_plan_string"]
+            "bsg_plan_string", *_MOE_OPS, *("bsg_validate_" + n for n in _MOE_OPS), "bsg_moe_rows"]
 
 
 def _ptr(t):
@@ -432,7 +448,8 @@ def gemm_proj_rope_mxfp8(x, w, x_scale, w_scale, cos, sin, out_fp8_row, out_scal
 # ---------------------------------------------------------------------------
 def workspace_bytes(name, m, n, k) -> int:
     """Scratch bytes that operator `name` takes at these sizes (0 for
-    quant_i8).  A program keeps one such buffer beside its layer."""
+    quant_i8; moe_sort: of tokens, top_k, num_experts).  A program keeps one
+    such buffer beside its layer."""
     if name == "quant_i8":
         return 0
     if name not in _WS_OPS:
@@ -450,8 +467,8 @@ def _refuse_sizes(*sizes):
 def plan_string(name, m, n, k) -> str:
     """How operator `name` goes out at these sizes (see include/bsg.h): for
     tests and tuning."""
-    if name not in _WS_OPS:
-        raise ValueError(f"no operator named {name!r}")
+    if name not in _WS_OPS or name == "moe_sort":
+        raise ValueError(f"no product named {name!r}")
     s = lib().bsg_plan_string(_WS_OPS[name], m, n, k)
     if s is None:
         _refuse_sizes(m, n, k)
@@ -577,3 +594,178 @@ def gemm_glu_bwd(dh, x, w_gate, w_up, g, u, dx, dw_gate, dw_up, m, n, k, act="si
     if validate_only:
         return lib().bsg_validate_gemm_glu_bwd(*args)
     _check(lib().gemm_glu_bwd(*args, _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# Expert operators
+# ---------------------------------------------------------------------------
+_I32 = torch.int32
+_FP8 = {"e4m3": (E4M3, torch.float8_e4m3fn), "e5m2": (E5M2, torch.float8_e5m2)}
+
+
+def _fp8(fmt):
+    """The bsg_dtype code of an 8-bit float format's name."""
+    if fmt not in _FP8:
+        raise ValueError(f"an 8-bit float format is one of {sorted(_FP8)}, got {fmt!r}")
+    return _FP8[fmt][0]
+
+
+def _codes_of(t, fmt):
+    """The dtype that a tensor of codes has to have: the format's own, or bytes."""
+    _fp8(fmt)
+    return torch.uint8 if isinstance(t, torch.Tensor) and t.dtype is torch.uint8 else _FP8[fmt][1]
+
+
+def moe_rows(tokens, top_k, num_experts) -> int:
+    """Rows that any routing of these sizes fits in, each expert's range
+    padded to 256 (see include/bsg.h)."""
+    m = lib().bsg_moe_rows(tokens, top_k, num_experts)
+    if m < 0:
+        raise BsgError(2 if tokens < 0 or top_k < 1 or not 1 <= num_experts <= 1024 else 5, lib().bsg_last_error().decode())
+    return m
+
+
+def moe_sort(expert, padded_offsets, expert_rows, row_of, pair_of, tokens, top_k, num_experts, m, workspace=None,
+             stream=None, validate_only=False):
+    """Expert ids (tokens, top_k) -> the order of the rows: padded_offsets and
+    expert_rows (num_experts,), row_of (tokens, top_k) and pair_of (m,), which
+    may be None (see include/bsg.h).  m: at least moe_rows(...)."""
+    pairs = 4 * tokens * top_k
+    args = _addresses((expert, "expert", pairs, _I32), (padded_offsets, "padded_offsets", 4 * num_experts, _I32),
+                      (expert_rows, "expert_rows", 4 * num_experts, _I32), (row_of, "row_of", pairs, _I32),
+                      (pair_of, "pair_of", 4 * m, _I32), (workspace, "workspace", 0, None))
+    args += (_ws_bytes(workspace, "moe_sort", tokens, top_k, num_experts), tokens, top_k, num_experts, m)
+    if validate_only:
+        return lib().bsg_validate_moe_sort(*args)
+    _check(lib().moe_sort(*args, _stream(stream)))
+
+
+def moe_gather(x, row_of, padded_offsets, expert_rows, weight, y, scale, prob, tokens, hidden, top_k, num_experts, m,
+               zero_pad=True, x_dtype=None, y_dtype=None, stream=None, validate_only=False):
+    """y[row_of[t, j]] = x[t] and prob[row_of[t, j]] = weight[t, j] (see
+    include/bsg.h).  y has x's type, or 8-bit codes (y_dtype "e4m3", taken from
+    a float8_e4m3fn y) with scale (ceil(hidden / 128), m).  weight and prob may
+    be None.  zero_pad: rows of an expert's range without a pair become zeros."""
+    xd = _code(x_dtype, x)
+    yd = _d_code(y_dtype, y) if y_dtype is not None or isinstance(y, torch.Tensor) else xd
+    out = _codes_of(y, "e4m3") if yd == E4M3 else _TORCH_OF.get(yd)
+    pairs = 4 * tokens * top_k
+    args = _addresses((x, "x", _out_bytes(xd, tokens * hidden), _TORCH_OF.get(xd)), (row_of, "row_of", pairs, _I32),
+                      (padded_offsets, "padded_offsets", 4 * num_experts, _I32),
+                      (expert_rows, "expert_rows", 4 * num_experts, _I32), (weight, "weight", pairs, _F32),
+                      (y, "y", _out_bytes(yd, m * hidden), out), (scale, "scale", 4 * m * _cdiv(hidden, 128), _F32),
+                      (prob, "prob", 4 * m, _F32))
+    args += (tokens, hidden, top_k, num_experts, m, int(bool(zero_pad)), xd, yd)
+    if validate_only:
+        return lib().bsg_validate_moe_gather(*args)
+    _check(lib().moe_gather(*args, _stream(stream)))
+
+
+def moe_gather_bwd(dy, dprob, row_of, dx, dweight, tokens, hidden, top_k, m, dtype=None, stream=None,
+                   validate_only=False):
+    """Gradients of moe_gather: dx[t] = sum_j dy[row_of[t, j]] and dweight[t, j]
+    = dprob[row_of[t, j]] (see include/bsg.h).  dprob and dweight, or dy and dx,
+    may be None."""
+    dt = _code(dtype, dx if dtype is None and dx is not None else dy) if dx is not None or dy is not None or dtype is not None else F32
+    td, pairs = _TORCH_OF.get(dt), 4 * tokens * top_k
+    args = _addresses((dy, "dy", _out_bytes(dt, m * hidden), td), (dprob, "dprob", 4 * m, _F32),
+                      (row_of, "row_of", pairs, _I32), (dx, "dx", _out_bytes(dt, tokens * hidden), td),
+                      (dweight, "dweight", pairs, _F32))
+    args += (tokens, hidden, top_k, m, dt)
+    if validate_only:
+        return lib().bsg_validate_moe_gather_bwd(*args)
+    _check(lib().moe_gather_bwd(*args, _stream(stream)))
+
+
+def moe_combine(y, row_of, weight, out, tokens, hidden, top_k, m, dtype=None, stream=None, validate_only=False):
+    """out[t] = sum_j weight[t, j] y[row_of[t, j]] (see include/bsg.h); weight
+    None: ones."""
+    dt = _code(dtype, out)
+    td, pairs = _TORCH_OF.get(dt), 4 * tokens * top_k
+    args = _addresses((y, "y", _out_bytes(dt, m * hidden), td), (row_of, "row_of", pairs, _I32),
+                      (weight, "weight", pairs, _F32), (out, "out", _out_bytes(dt, tokens * hidden), td))
+    args += (tokens, hidden, top_k, m, dt)
+    if validate_only:
+        return lib().bsg_validate_moe_combine(*args)
+    _check(lib().moe_combine(*args, _stream(stream)))
+
+
+def moe_combine_bwd(dout, y, row_of, padded_offsets, expert_rows, weight, dy, dweight, tokens, hidden, top_k,
+                    num_experts, m, zero_pad=True, dtype=None, stream=None, validate_only=False):
+    """Gradients of moe_combine: dy[row_of[t, j]] = weight[t, j] dout[t] and
+    dweight[t, j] = <dout[t], y[row_of[t, j]]> (see include/bsg.h).  dy, or
+    dweight and y, may be None."""
+    dt = _code(dtype, dout)
+    td, pairs, rows = _TORCH_OF.get(dt), 4 * tokens * top_k, _out_bytes(dt, m * hidden)
+    args = _addresses((dout, "dout", _out_bytes(dt, tokens * hidden), td), (y, "y", rows, td),
+                      (row_of, "row_of", pairs, _I32), (padded_offsets, "padded_offsets", 4 * num_experts, _I32),
+                      (expert_rows, "expert_rows", 4 * num_experts, _I32), (weight, "weight", pairs, _F32),
+                      (dy, "dy", rows, td), (dweight, "dweight", pairs, _F32))
+    args += (tokens, hidden, top_k, num_experts, m, int(bool(zero_pad)), dt)
+    if validate_only:
+        return lib().bsg_validate_moe_combine_bwd(*args)
+    _check(lib().moe_combine_bwd(*args, _stream(stream)))
+
+
+def quant_fp8(x, q, scale, q_t, scale_t, m, k, l=1, tile=False, q_dtype="e4m3", x_dtype=None, stream=None,
+              validate_only=False):
+    """x (l, m, k) -> 8-bit floats with a scale for each 128 values along k (q,
+    scale) and along m (q_t, transposed, and scale_t), or with tile for each 128
+    x 128 (see include/bsg.h).  Either pair may be None."""
+    xd, qd, mb, kb = _code(x_dtype, x), _fp8(q_dtype), _cdiv(m, 128), _cdiv(k, 128)
+    args = _addresses((x, "x", _out_bytes(xd, l * m * k), _TORCH_OF.get(xd)),
+                      (q, "q", l * m * k, _codes_of(q, q_dtype)), (scale, "scale", 4 * l * kb * (mb if tile else m), _F32),
+                      (q_t, "q_t", l * m * k, _codes_of(q_t, q_dtype)),
+                      (scale_t, "scale_t", 4 * l * mb * (kb if tile else k), _F32))
+    args += (l, m, k, int(bool(tile)), xd, qd)
+    if validate_only:
+        return lib().bsg_validate_quant_fp8(*args)
+    _check(lib().quant_fp8(*args, _stream(stream)))
+
+
+def gemm_fp8(a, b, a_scale, b_scale, c, m, n, k, a_dtype="e4m3", c_dtype=None, workspace=None, stream=None,
+             validate_only=False):
+    """c = a b^T from 8-bit floats with a scale for each 128 of k (a: each row,
+    b: each 128 rows; see include/bsg.h)."""
+    cd, kb = _code(c_dtype, c), _cdiv(k, 128)
+    args = _addresses((a, "a", m * k, _codes_of(a, a_dtype)), (b, "b", n * k, _codes_of(b, "e4m3")),
+                      (a_scale, "a_scale", 4 * kb * m, _F32), (b_scale, "b_scale", 4 * kb * _cdiv(n, 128), _F32),
+                      (c, "c", _out_bytes(cd, m * n), _TORCH_OF.get(cd)), (workspace, "workspace", 0, None))
+    args += (_ws_bytes(workspace, "gemm_fp8", m, n, k), m, n, k, _fp8(a_dtype), cd)
+    if validate_only:
+        return lib().bsg_validate_gemm_fp8(*args)
+    _check(lib().gemm_fp8(*args, _stream(stream)))
+
+
+def grouped_gemm_fp8(a, b, a_scale, b_scale, padded_offsets, expert_rows, c, m, n, k, num_experts, max_rows=0,
+                     a_dtype="e4m3", c_dtype=None, stream=None, validate_only=False):
+    """gemm_fp8 of rows sorted by expert with a weight for each expert (see
+    include/bsg.h).  expert_rows may be None; max_rows: no expert has more rows
+    (0: not known), for the choice of the kernel."""
+    cd, kb = _code(c_dtype, c), _cdiv(k, 128)
+    args = _addresses((a, "a", m * k, _codes_of(a, a_dtype)), (b, "b", num_experts * n * k, _codes_of(b, "e4m3")),
+                      (a_scale, "a_scale", 4 * kb * m, _F32),
+                      (b_scale, "b_scale", 4 * num_experts * kb * _cdiv(n, 128), _F32),
+                      (padded_offsets, "padded_offsets", 4 * num_experts, _I32),
+                      (expert_rows, "expert_rows", 4 * num_experts, _I32),
+                      (c, "c", _out_bytes(cd, m * n), _TORCH_OF.get(cd)))
+    args += (m, n, k, num_experts, max_rows, _fp8(a_dtype), cd)
+    if validate_only:
+        return lib().bsg_validate_grouped_gemm_fp8(*args)
+    _check(lib().grouped_gemm_fp8(*args, _stream(stream)))
+
+
+def grouped_gemm_fp8_wgrad(a, b, a_scale, b_scale, padded_offsets, c, m, n, k, num_experts, a_dtype="e4m3",
+                           c_dtype=None, stream=None, validate_only=False):
+    """Gradient of the experts' weights, c (num_experts, n, k), from the
+    transposed codes of the output's gradient, a (n, m), and of the input, b
+    (k, m) (see include/bsg.h)."""
+    cd, mb = _code(c_dtype, c), _cdiv(m, 128)
+    args = _addresses((a, "a", n * m, _codes_of(a, a_dtype)), (b, "b", k * m, _codes_of(b, "e4m3")),
+                      (a_scale, "a_scale", 4 * mb * n, _F32), (b_scale, "b_scale", 4 * mb * _cdiv(k, 128), _F32),
+                      (padded_offsets, "padded_offsets", 4 * num_experts, _I32),
+                      (c, "c", _out_bytes(cd, num_experts * n * k), _TORCH_OF.get(cd)))
+    args += (m, n, k, num_experts, _fp8(a_dtype), cd)
+    if validate_only:
+        return lib().bsg_validate_grouped_gemm_fp8_wgrad(*args)
+    _check(lib().grouped_gemm_fp8_wgrad(*args, _stream(stream)))

@@ -20,8 +20,8 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall", "-Wno
 
 
 def sources():
-    return sorted(os.path.join(d, f) for d in (CSRC, os.path.join(CSRC, "ffn")) for f in os.listdir(d)
-                  if f.endswith((".hip", ".cpp")))
+    dirs = [CSRC, os.path.join(CSRC, "ffn"), os.path.join(CSRC, "moe")]
+    return sorted(os.path.join(d, f) for d in dirs for f in os.listdir(d) if f.endswith((".hip", ".cpp")))
 
 
 def _compile(src: str) -> str:

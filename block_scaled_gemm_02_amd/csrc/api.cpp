@@ -6,68 +6,18 @@
 // (Scheduling, caching, and errors).  Device-resident values are not read.
 #include <hip/hip_runtime.h>
 
-#include <cstdarg>
 #include <cstdio>
-#include <cstring>
 #include <utility>
 
-#include "../../include/bsg.h"
+#include "api.hpp"
 #include "ffn/ffn.hpp"
 #include "ffn/plan.hpp"
+#include "moe/moe.hpp"
 #include "launch.hpp"
 
+using namespace bsg::api;
+
 namespace {
-
-thread_local char g_err[512] = "";
-
-int fail(int status, const char *fmt, ...)
-{
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(g_err, sizeof g_err, fmt, ap);
-    va_end(ap);
-    return status;
-}
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int elem_bytes(int dt)
-{
-    switch (dt) {
-    case BSG_F32: return 4;
-    case BSG_F16:
-    case BSG_BF16: return 2;
-    default: return 1;
-    }
-}
-
-bool is_float_out(int dt) { return dt == BSG_F32 || dt == BSG_F16 || dt == BSG_BF16; }
-
-// Device check: the kernels are built for gfx950 only.
-int check_device()
-{
-    static int cached[64];   // 0 unknown, 1 ok, 2 bad
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess) return fail(BSG_ERR_DEVICE, "hipGetDevice failed");
-    if (dev >= 0 && dev < 64 && cached[dev] == 1) return BSG_OK;
-    hipDeviceProp_t prop;
-    if (hipGetDeviceProperties(&prop, dev) != hipSuccess)
-        return fail(BSG_ERR_DEVICE, "hipGetDeviceProperties failed");
-    if (std::strncmp(prop.gcnArchName, "gfx950", 6) != 0) {
-        if (dev >= 0 && dev < 64) cached[dev] = 2;
-        return fail(BSG_ERR_DEVICE, "device %d is %s; this library is built for gfx950", dev,
-                    prop.gcnArchName);
-    }
-    if (dev >= 0 && dev < 64) cached[dev] = 1;
-    return BSG_OK;
-}
-
-int launch_status(hipError_t e, const char *what)
-{
-    if (e == hipSuccess) return BSG_OK;
-    if (e == hipErrorNotSupported) return fail(BSG_ERR_UNSUPPORTED, "%s: not supported", what);
-    return fail(BSG_ERR_LAUNCH, "%s: launch failed: %s", what, hipGetErrorString(e));
-}
 
 int check_ab_sf(int ab_dtype, int sf_vec_size)
 {
@@ -588,42 +538,11 @@ int gemm_proj_rope_mxfp8(const void *x, const void *w, const uint8_t *x_scale, c
 // int32 sums of products of int8 are exact up to this K: 2^14 k < 2^31
 static constexpr int64_t kMaxI8K = 131056;
 
-static int check_ffn_sizes(int64_t m, int64_t n, int64_t k)
-{
-    if (m < 0 || n < 0 || k < 0) return fail(BSG_ERR_SHAPE, "negative size");
-    if (m > (1ll << 22) || n > (1ll << 20) || k > (1ll << 20))
-        return fail(BSG_ERR_UNSUPPORTED, "M=%lld, N=%lld, K=%lld: past 2^22 tokens or 2^20 channels", (long long)m,
-                    (long long)n, (long long)k);
-    return BSG_OK;
-}
-
-// output tiles of an (r, c) product: the grid's limit
-static int check_ffn_tiles(int64_t r, int64_t c)
-{
-    const int64_t tiles = ((r + 63) / 64) * ((c + 63) / 64);
-    if (tiles >= (1ll << 23)) return fail(BSG_ERR_UNSUPPORTED, "%lld output tiles exceed the launch limit", (long long)tiles);
-    return BSG_OK;
-}
-
 static int check_act(int act)
 {
     if (act < BSG_ACT_SILU || act > BSG_ACT_RELU) return fail(BSG_ERR_SHAPE, "act %d is not a bsg_act", act);
     return BSG_OK;
 }
-
-static int check_workspace(const void *ws, int64_t have, int op, int64_t m, int64_t n, int64_t k)
-{
-    const int64_t need = bsg_workspace_bytes(op, m, n, k);
-    if (need == 0) return BSG_OK;
-    if (!ws) return fail(BSG_ERR_NULLPTR, "a workspace of %lld bytes is required", (long long)need);
-    if (!aligned16(ws)) return fail(BSG_ERR_ALIGN, "workspace must be 16-byte aligned");
-    if (have < need)
-        return fail(BSG_ERR_SHAPE, "workspace holds %lld bytes; these sizes need %lld", (long long)have, (long long)need);
-    return BSG_OK;
-}
-
-static bool is_16bit(int dt) { return dt == BSG_F16 || dt == BSG_BF16; }
-static bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 int64_t bsg_workspace_bytes(int op, int64_t m, int64_t n, int64_t k)
 {
@@ -633,6 +552,8 @@ int64_t bsg_workspace_bytes(int op, int64_t m, int64_t n, int64_t k)
     case BSG_OP_GEMM_GLU: return bsg::ffn::workspace_gemm_glu(m, n, k, false);
     case BSG_OP_GEMM_GLU_I8: return bsg::ffn::workspace_gemm_glu(m, n, k, true);
     case BSG_OP_GEMM_GLU_BWD: return bsg::ffn::workspace_gemm_glu_bwd(m, n, k);
+    case BSG_OP_MOE_SORT: return bsg_moe_rows(m, n, k) < 0 ? -1 : bsg::moe::workspace_moe_sort(m * n, k);
+    case BSG_OP_GEMM_FP8: return bsg::moe::workspace_gemm_fp8(m, n, k);
     default: fail(BSG_ERR_SHAPE, "op %d is not a bsg_op", op); return -1;
     }
 }

@@ -1,0 +1,221 @@
+// Rows of tokens into expert order and back (moe_gather, moe_combine and
+// their gradients).  A map, row_of (tokens, top_k), says which row holds a
+// token's choice j, or -1; every row belongs to one pair at most, so all sums
+// run over a token's own choices, in their order, and nothing is added
+// atomically.
+#include "rows.hpp"
+
+namespace bsg {
+namespace moe {
+namespace {
+
+// The row of a token's choice, or -1 for none: what is not in [0, m) is none.
+__device__ __forceinline__ int row_at(const int32_t *row_of, int64_t pair, int64_t m)
+{
+    const int r = row_of[pair];
+    return (uint64_t)(uint32_t)r < (uint64_t)m ? r : -1;
+}
+
+// Rows of an expert that hold no pair, a quarter of the most there can be for
+// each workgroup that is added for them.
+struct Pad {
+    int64_t first, last;
+};
+__device__ __forceinline__ Pad pad_of(int b, const int32_t *padded_offsets, const int32_t *expert_rows, int64_t m)
+{
+    const int e = b / 4, q = b % 4;
+    const int64_t begin = e ? padded_offsets[e - 1] : 0, end = min((int64_t)padded_offsets[e], m);
+    const int64_t first = begin + expert_rows[e] + 64 * q;
+    return {max((int64_t)0, first), min(end, first + 64)};
+}
+
+// Copies 16-byte pieces of rows.
+__global__ __launch_bounds__(256) void k_gather(GatherArgs p, int lg, unsigned rows_grid, int64_t pieces)
+{
+    const int per = 256 >> lg, sub = threadIdx.x >> lg;
+    const int64_t col = ((int64_t)blockIdx.y << lg) + (threadIdx.x & ((1 << lg) - 1));
+    u32x4 *const y = (u32x4 *)p.y;
+    if (blockIdx.x >= rows_grid) {
+        const Pad d = pad_of(blockIdx.x - rows_grid, p.padded_offsets, p.expert_rows, p.m);
+        for (int64_t r = d.first + sub; r < d.last; r += per) {
+            if (col < pieces) y[r * pieces + col] = u32x4{0, 0, 0, 0};
+            if (col == 0 && p.prob) p.prob[r] = 0.0f;
+        }
+        return;
+    }
+    const int64_t t = (int64_t)blockIdx.x * per + sub;
+    if (t >= p.tokens || col >= pieces) return;
+    const u32x4 x = ((const u32x4 *)p.x)[t * pieces + col];
+    for (int j = 0; j < p.top_k; ++j) {
+        const int r = row_at(p.row_of, t * p.top_k + j, p.m);
+        if (r < 0) continue;
+        y[r * pieces + col] = x;
+        if (col == 0 && p.prob) p.prob[r] = p.weight[t * p.top_k + j];
+    }
+}
+
+// Quantises pieces of 8 elements on their way; 16 lanes hold a group of 128.
+template <int DT>
+__global__ __launch_bounds__(256) void k_gather_fp8(GatherArgs p, int lg, unsigned rows_grid, int64_t pieces)
+{
+    const int per = 256 >> lg, sub = threadIdx.x >> lg;
+    const int64_t col = ((int64_t)blockIdx.y << lg) + (threadIdx.x & ((1 << lg) - 1));
+    u32x2 *const y = (u32x2 *)p.y;
+    const bool first = (col & 15) == 0 && col < pieces;         // of a group
+    float *const sc = p.scale + (col >> 4) * p.m;
+    if (blockIdx.x >= rows_grid) {
+        const Pad d = pad_of(blockIdx.x - rows_grid, p.padded_offsets, p.expert_rows, p.m);
+        const float least = scale_of<false>(0).scale;
+        for (int64_t r = d.first + sub; r < d.last; r += per) {
+            if (col < pieces) y[r * pieces + col] = u32x2{0, 0};
+            if (first) sc[r] = least;
+            if (col == 0 && p.prob) p.prob[r] = 0.0f;
+        }
+        return;
+    }
+    const int64_t t = (int64_t)blockIdx.x * per + sub;
+    const bool in = t < p.tokens && col < pieces;
+    Piece<DT, 8> x;
+    x.zero();
+    if (in) x.load((const char *)p.x + (t * pieces + col) * 8 * es_dt(DT));
+    uint32_t top = x.top(0);
+#pragma unroll
+    for (int d = 8; d; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+    if (!in) return;
+    const Scale s = scale_of<false>(top);
+    const u32x2 q = {codes4<false>(x.at(0), x.at(1), x.at(2), x.at(3), s.inv, s.keep),
+                     codes4<false>(x.at(4), x.at(5), x.at(6), x.at(7), s.inv, s.keep)};
+    for (int j = 0; j < p.top_k; ++j) {
+        const int r = row_at(p.row_of, t * p.top_k + j, p.m);
+        if (r < 0) continue;
+        y[r * pieces + col] = q;
+        if (first) sc[r] = s.scale;
+        if (col == 0 && p.prob) p.prob[r] = p.weight[t * p.top_k + j];
+    }
+}
+
+// out[t] = sum_j weight[t, j] y[row_of[t, j]], in fp32, rounded once.
+template <int DT, bool WEIGHT>
+__global__ __launch_bounds__(256) void k_combine(CombineArgs p, int lg, int64_t pieces)
+{
+    constexpr int N = 16 / es_dt(DT);
+    const int64_t col = ((int64_t)blockIdx.y << lg) + (threadIdx.x & ((1 << lg) - 1));
+    const int64_t t = (int64_t)blockIdx.x * (256 >> lg) + (threadIdx.x >> lg);
+    if (t >= p.tokens) return;
+    if constexpr (!WEIGHT) {
+        if (p.dweight && blockIdx.y == 0)
+            for (int j = threadIdx.x & ((1 << lg) - 1); j < p.top_k; j += 1 << lg) {
+                const int r = row_at(p.row_of, t * p.top_k + j, p.m);
+                p.dweight[t * p.top_k + j] = r < 0 ? 0.0f : p.dprob[r];
+            }
+    }
+    if (col >= pieces || !p.out) return;
+    float acc[N] = {};
+    for (int j = 0; j < p.top_k; ++j) {
+        const int r = row_at(p.row_of, t * p.top_k + j, p.m);
+        if (r < 0) continue;
+        Piece<DT, N> y;
+        y.load((const u32x4 *)p.y + r * pieces + col);
+        const float w = WEIGHT ? p.weight[t * p.top_k + j] : 1.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] = WEIGHT ? fmaf(w, y.at(i), acc[i]) : acc[i] + y.at(i);
+    }
+    ((u32x4 *)p.out)[t * pieces + col] = pack16<DT>(acc);
+}
+
+// dy[row] = weight dout[t] and dweight = <dout[t], y[row]>.
+template <int DT>
+__global__ __launch_bounds__(256) void k_combine_bwd(CombineBwdArgs p, int lg, unsigned rows_grid, int64_t pieces)
+{
+    constexpr int N = 16 / es_dt(DT);
+    const int tpr = 1 << lg, per = 256 >> lg, sub = threadIdx.x >> lg, c0 = threadIdx.x & (tpr - 1);
+    u32x4 *const dy = (u32x4 *)p.dy;
+    if (blockIdx.x >= rows_grid) {
+        const Pad d = pad_of(blockIdx.x - rows_grid, p.padded_offsets, p.expert_rows, p.m);
+        for (int64_t r = d.first + sub; r < d.last; r += per)
+            for (int64_t c = c0; c < pieces; c += tpr) dy[r * pieces + c] = u32x4{0, 0, 0, 0};
+        return;
+    }
+    __shared__ float part[4];
+    const int64_t t = (int64_t)blockIdx.x * per + sub;
+    const bool in = t < p.tokens;
+    for (int j = 0; j < p.top_k; ++j) {
+        const int64_t pair = t * p.top_k + j;
+        const int r = in ? row_at(p.row_of, pair, p.m) : -1;
+        const float w = r >= 0 ? p.weight[pair] : 0.0f;
+        float dot = 0.0f;
+        if (r >= 0)
+            for (int64_t c = c0; c < pieces; c += tpr) {
+                Piece<DT, N> d, y;
+                d.load((const u32x4 *)p.dout + t * pieces + c);
+                if (p.dweight) {
+                    y.load((const u32x4 *)p.y + r * pieces + c);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) dot = fmaf(d.at(i), y.at(i), dot);
+                }
+                if (dy) {
+                    float o[N];
+#pragma unroll
+                    for (int i = 0; i < N; ++i) o[i] = w * d.at(i);
+                    dy[r * pieces + c] = pack16<DT>(o);
+                }
+            }
+        if (!p.dweight) continue;
+        for (int d = min(tpr, 64) / 2; d; d >>= 1) dot += __shfl_xor(dot, d);
+        if (tpr > 64) {
+            __syncthreads();
+            if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = dot;
+            __syncthreads();
+            dot = tpr == 128 ? part[2 * sub] + part[2 * sub + 1] : (part[0] + part[1]) + (part[2] + part[3]);
+        }
+        if (in && c0 == 0) p.dweight[pair] = dot;
+    }
+}
+
+}  // namespace
+
+hipError_t launch_moe_gather(const GatherArgs &a, hipStream_t s)
+{
+    const unsigned pads = a.zero_pad ? 4u * (unsigned)a.num_experts : 0u;
+    if (a.y_dtype == DT_E4M3) {
+        const int64_t pieces = a.hidden / 8;
+        const Lay l = lay_of(a.tokens, pieces, 4);
+        if (l.rows + pads == 0) return hipSuccess;
+        with_float(a.x_dtype, [&](auto dt) {
+            k_gather_fp8<decltype(dt)::value><<<dim3(l.rows + pads, l.cols), 256, 0, s>>>(a, l.lg, l.rows, pieces);
+        });
+    } else {
+        const int64_t pieces = a.hidden * es_dt(a.x_dtype) / 16;
+        const Lay l = lay_of(a.tokens, pieces, 4);
+        if (l.rows + pads == 0) return hipSuccess;
+        k_gather<<<dim3(l.rows + pads, l.cols), 256, 0, s>>>(a, l.lg, l.rows, pieces);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_moe_combine(const CombineArgs &a, hipStream_t s)
+{
+    if (a.tokens == 0) return hipSuccess;
+    const int64_t pieces = a.hidden * es_dt(a.dtype) / 16;
+    const Lay l = lay_of(a.tokens, pieces, 4);
+    with_float(a.dtype, [&](auto dt) {
+        if (a.weight) k_combine<decltype(dt)::value, true><<<dim3(l.rows, l.cols), 256, 0, s>>>(a, l.lg, pieces);
+        else k_combine<decltype(dt)::value, false><<<dim3(l.rows, l.cols), 256, 0, s>>>(a, l.lg, pieces);
+    });
+    return hipGetLastError();
+}
+
+hipError_t launch_moe_combine_bwd(const CombineBwdArgs &a, hipStream_t s)
+{
+    const unsigned pads = a.zero_pad && a.dy ? 4u * (unsigned)a.num_experts : 0u;
+    const int64_t pieces = a.hidden * es_dt(a.dtype) / 16;
+    const Lay l = lay_of(a.tokens, pieces, 4);
+    if (l.rows + pads == 0) return hipSuccess;
+    with_float(a.dtype, [&](auto dt) {
+        k_combine_bwd<decltype(dt)::value><<<l.rows + pads, 256, 0, s>>>(a, l.lg, l.rows, pieces);
+    });
+    return hipGetLastError();
+}
+
+}  // namespace moe
+}  // namespace bsg
