@@ -13,6 +13,7 @@
 #include "ffn/ffn.hpp"
 #include "ffn/plan.hpp"
 #include "moe/moe.hpp"
+#include "moe/plan.hpp"
 #include "launch.hpp"
 
 using namespace bsg::api;
@@ -584,8 +585,15 @@ const char *bsg_plan_string(int op, int64_t m, int64_t n, int64_t k)
         else if (x && w) snprintf(text, sizeof text, "dX: %s, dW: %s", Name(p.x).s, Name(p.w).s);
         else if (x || w) snprintf(text, sizeof text, "%s: %s", x ? "dX" : "dW", Name(x ? p.x : p.w).s);
         else return "none";
+    } else if (op == BSG_OP_GEMM_FP8) {
+        if (!m || !n) return "none";
+        const bsg::moe::Plan p = bsg::moe::plan_gemm_fp8(m, n, k);
+        static const char *const shape[3] = {"Big", "Mid", "Small"};
+        if (p.few) snprintf(text, sizeof text, "few %d", p.few);
+        else if (p.splits > 1) snprintf(text, sizeof text, "%s / %d", shape[p.shape], p.splits);
+        else snprintf(text, sizeof text, "%s", shape[p.shape]);
     } else {
-        fail(BSG_ERR_SHAPE, "op %d is not a bsg_op", op);
+        fail(BSG_ERR_SHAPE, "op %d is not a product", op);
         return nullptr;
     }
     return text;

@@ -43,37 +43,58 @@ __device__ __forceinline__ f32x4 mfma128(const i32x8 &b, const i32x8 &a)
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, zero, 0, AE5 ? 1 : 0, 0, 0, 0, 0);
 }
 
-// One tile's operands: row 0, column 0, K block 0.
+// What the loads of a tile take: its rows of A and of B, A's scales, and the
+// bytes of its K range.  (row 0, K block 0)
+struct Source {
+    i32x4 ra, rb;
+    const float *sa;
+    uint32_t klimit, rows;
+};
+// And what its way out takes.
+struct Place {
+    char *c;                    // row 0, column 0
+    const float *sb;            // of the first 128 columns
+    int rows, cols;
+};
 struct Part {
-    const uint8_t *a, *b;
-    const float *sa, *sb;
-    int64_t lda, ldb, sa_ld, sb_ld;
-    int64_t k;
-    int rows, held, cols;       // of C; rows of A that count
-    char *c;
+    Source src;
+    Place to;
 };
 
-template <int WM_, int WN_, int GM_, int GN_, int S_>
+// SUMS: leaves fp32 sums (a part of K) instead of C.
+template <int WM_, int WN_, int GM_, int GN_, int S_, bool SUMS_ = false>
 struct Fp8Tile {
     static constexpr int WM = WM_, WN = WN_, GM = GM_, GN = GN_, S = S_;
+    static constexpr bool SUMS = SUMS_;
+    typedef Fp8Tile<WM, WN, GM, GN, S, true> Sums;
     static constexpr int TM = 16 * WM * GM, TN = 16 * WN * GN, W = GM * GN, kThreads = 64 * W;
-    static constexpr int kA = TM * 128, kB = TN * 128, kSlot = kA + kB + 256 * W, kLds = S * kSlot;
-    static constexpr int LA = TM / 8 / W, LB = TN / 8 / W, L = LA + LB + 1;      // loads of a wave and block
-    static constexpr int RW = TM / W;                                            // rows whose scales a wave loads
-    static constexpr int kWaves = W * (160 * 1024 / kLds) / 4 > 0 ? W * (160 * 1024 / kLds) / 4 : 1;
-    static constexpr int kStage = kLds / W & ~15;
+    static constexpr int kA = TM * 128, kB = TN * 128, kSlot = kA + kB + 256 * W;
+    static constexpr int RB = 32 * WN, kRow = RB + 16, kStage = 16 * kRow;      // 16 rows of C on their way out
+    static constexpr int kLds = S * kSlot + (SUMS ? 0 : W * kStage);
+    static constexpr int LA = TM / 8 / W, LB = TN / 8 / W, L = LA + LB + 1;     // loads of a wave and block
+    static constexpr int RW = TM / W;                                           // rows whose scales a wave loads
+    static constexpr int kGroups = 160 * 1024 / kLds;                           // workgroups a compute unit
+    static constexpr int kWaves = W * kGroups / 4 > 0 ? W * kGroups / 4 : 1;
+    static constexpr int C = WM < 4 ? WM : 4;                                   // scales a read
+    // Fragments in registers: two whole blocks', or (kAhead rows ahead) those of
+    // one block's columns and kRing of its rows, where two do not fit.
+    static constexpr bool WHOLE = WM < 4;
+    static constexpr int kRing = WHOLE ? WM : 4, kAhead = WHOLE ? WM : 3;
+    static constexpr int kMin = WHOLE ? (S + 1) / 2 * 2 : S;                    // least blocks of a tile
+    static constexpr int N = WM * WN;
     static_assert(128 % (16 * WN) == 0, "a wave's columns lie in one 128");
-    static_assert(LA * 8 * W == TM && LB * 8 * W == TN && RW <= 64 && RW % WM == 0 && WM >= 2, "whole loads");
-    static constexpr int kRing = WM % 4 == 0 ? 4 : 2, kAhead = kRing / 2;        // A fragments in registers
+    static_assert(LA * 8 * W == TM && LB * 8 * W == TN && RW <= 64 && RW % C == 0 && WM >= 2, "whole loads");
+    static_assert(64 % (2 * WN) == 0 && 16 % (32 / WN) == 0, "whole rows a store");
 
-    const Part &p;
     uint8_t *const lds;
     int lane, w, wm, wn;
-    uint32_t voff_a, voff_b, voff_s, chunk, klimit;
-    i32x4 ra, rb;
-    uint32_t rd_a[2], rd_b[2], rd_s;
+    uint32_t ld, chunk, voff, voff_s;
+    int64_t sa_ld;
+    uint32_t rd_a[2], rd_b[2], rd_s[WM / C];
+    int at;                     // the slot of the block at work
 
-    __device__ __forceinline__ Fp8Tile(const Part &part, uint8_t *ring) : p(part), lds(ring)
+    // ld: bytes of a row of A and of B; sa_ld: between A's scales of two blocks
+    __device__ __forceinline__ Fp8Tile(uint8_t *ring, int64_t ld, int64_t sa_ld) : lds(ring), ld((uint32_t)ld), sa_ld(sa_ld), at(0)
     {
         lane = threadIdx.x & 63;
         w = ffn::wave_id();
@@ -82,13 +103,13 @@ struct Fp8Tile {
         // loads: 8 rows of 128 bytes each
         const uint32_t row = (uint32_t)lane >> 3;
         chunk = 16 * (((uint32_t)lane & 7) ^ ffn::k_swizzle(row));
-        voff_a = row * (uint32_t)p.lda + chunk;
-        voff_b = row * (uint32_t)p.ldb + chunk;
-        klimit = (uint32_t)p.k;
-        ra = make_rsrc_words(p.a, ffn::clamp_bytes(p.held * p.lda));
-        rb = make_rsrc_words(p.b, ffn::clamp_bytes(p.cols * p.ldb));
-        const int q = w * RW + lane, at = q % (16 * WM);
-        voff_s = lane < RW ? 4u * (uint32_t)(q - at + 16 * (at % WM) + at / WM) : kOOB;
+        voff = row * (uint32_t)ld + chunk;
+        // scales: the wave's RW of the tile's TM go to the banks that its neighbours'
+        // leave, in the order (i / C, r, i % C) of rows 16 i + r, so that a read of C
+        // for each r meets every bank once
+        const int sub = w % (64 / RW), q = w * RW + lane - sub * RW, o = q % (16 * WM);
+        const int i = o / (16 * C) * C + o % C;
+        voff_s = lane / RW == sub ? 4u * (uint32_t)(q - o + 16 * i + o / C % 16) : kOOB;
         // fragment reads
         const uint32_t r = (uint32_t)lane & 15, g = (uint32_t)lane >> 4;
 #pragma unroll
@@ -97,122 +118,243 @@ struct Fp8Tile {
             rd_a[h] = (16u * WM * wm + r) * 128u + c;
             rd_b[h] = kA + (16u * WN * wn + r) * 128u + c;
         }
-        const uint32_t qr = 16u * WM * wm + r * WM;
-        rd_s = kA + kB + qr / RW * 256 + qr % RW * 4;
+#pragma unroll
+        for (int h = 0; h < WM / C; ++h) {
+            const uint32_t o = 16u * WM * wm + 16 * C * h + C * r, lw = o / RW;
+            rd_s[h] = kA + kB + lw * 256 + (lw % (64 / RW) * RW + o % RW) * 4;
+        }
     }
 
-    // Load Q of this wave's for K block kb, into the slot at lds + at.
+    // Load Q of this wave's for K block kb of a tile, into the slot at lds + to.
+    // Past the K range it reads nothing.
     template <int Q>
-    __device__ __forceinline__ void load(int at, int kb) const
+    __device__ __forceinline__ void load(const Source &s, int to, int kb) const
     {
         const uint32_t k = 128u * (uint32_t)kb;
         if constexpr (Q < LA + LB) {
-            const uint32_t add = k + chunk < klimit ? k : kOOB;
-            if constexpr (Q < LA)
-                lds_load16(ra, lds + at + 1024 * (LA * w + Q), voff_a + add + 8u * (LA * w + Q) * (uint32_t)p.lda);
-            else
-                lds_load16(rb, lds + at + kA + 1024 * (LB * w + Q - LA), voff_b + add + 8u * (LB * w + Q - LA) * (uint32_t)p.ldb);
+            const uint32_t v = k + chunk < s.klimit ? voff : kOOB;
+            if constexpr (Q < LA) lds_load16(s.ra, lds + to + 1024 * (LA * w + Q), v + (8u * (LA * w + Q) * ld + k));
+            else lds_load16(s.rb, lds + to + kA + 1024 * (LB * w + Q - LA), v + (8u * (LB * w + Q - LA) * ld + k));
         } else {
-            const i32x4 rs = make_rsrc_words(p.sa + kb * p.sa_ld, k < klimit ? 4u * (uint32_t)p.held : 0u);
-            lds_load4(rs, lds + at + kA + kB + 256 * w, voff_s);
+            const i32x4 rs = make_rsrc_words(s.sa + kb * sa_ld, k < s.klimit ? 4u * s.rows : 0u);
+            lds_load4(rs, lds + to + kA + kB + 256 * w, voff_s);
         }
     }
-    __device__ __forceinline__ i32x8 frag(int at, const uint32_t (&rd)[2], int off) const
+    __device__ __forceinline__ i32x8 frag(int from, const uint32_t (&rd)[2], int off) const
     {
-        const i32x4 x = *(const i32x4 *)(lds + at + rd[0] + off), y = *(const i32x4 *)(lds + at + rd[1] + off);
+        const i32x4 x = *(const i32x4 *)(lds + from + rd[0] + off), y = *(const i32x4 *)(lds + from + rd[1] + off);
         return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
     }
-
-    // acc = sum over the K blocks [kb0, kb0 + count), count >= 1.
-    template <bool AE5>
-    __device__ __forceinline__ void run(f32x4 (&acc)[WM][WN], int kb0, int count)
+    __device__ __forceinline__ void scales(int from, float (&o)[WM]) const
     {
-        const float *const sb = p.sb + (16 * WN * wn) / 128 * p.sb_ld;
-        const int sbn = (int)((p.k + 127) / 128);
+        typedef float V __attribute__((ext_vector_type(C)));
+#pragma unroll
+        for (int h = 0; h < WM / C; ++h) {
+            const V x = *(const V *)(lds + from + rd_s[h]);
+#pragma unroll
+            for (int c = 0; c < C; ++c) o[C * h + c] = x[c];
+        }
+    }
+
+    // A wave's fragments and scales at the border of two blocks.
+    struct Front {
+        i32x8 a[kRing], b[WN];
+        float raw[WM];
+    };
+
+    // The first S blocks of the first tile, and its front.
+    __device__ __forceinline__ void start(const Source &s, Front &f)
+    {
+        static_for<S>([&](auto n) {
+            static_for<L>([&](auto q) { load<decltype(q)::value>(s, decltype(n)::value * kSlot, decltype(n)::value); });
+        });
+        s_wait_vm<(S - 1) * L>();
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        scales(0, f.raw);
+#pragma unroll
+        for (int j = 0; j < WN; ++j) f.b[j] = frag(0, rd_b, 2048 * j);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) f.a[i] = frag(0, rd_a, 2048 * i);
+    }
+
+    // Blocks that run() is called for: whole steps, and as many as the ring has
+    // slots.  What is past the K range counts as zeros.
+    static __device__ __forceinline__ int count_of(int blocks)
+    {
+        return max(WHOLE ? (blocks + 1) & ~1 : blocks, kMin);
+    }
+
+    // acc = sum over the `count` blocks of a tile; leaves the front of the next
+    // tile's first block, whose loads come from `next`.  sb: B's scales of the
+    // wave's columns, nsb of them.
+    template <bool AE5>
+    __device__ __forceinline__ void run(f32x4 (&acc)[WM][WN], Front &fr, Source src, const Source &next, int count,
+                                        const float *sb, int nsb)
+    {
         // B's scales of 64 blocks, one a lane
-        float sbv = kb0 + lane < sbn ? sb[kb0 + lane] : 0.0f;
+        float sbv = lane < nsb ? sb[lane] : 0.0f;
         auto scale_b = [&](int i) { return __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(sbv), i & 63)); };
 #pragma unroll
         for (int i = 0; i < WM; ++i)
 #pragma unroll
             for (int j = 0; j < WN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-        s_wait_vm<0>();
-        // past the range a block reads nothing
-        auto block = [&](int i) { return i < count ? kb0 + i : 0x00800000; };
+        // t: results under way; the last three of a block are added in the next
+        // one, with the factors old of its last rows
+        float f[WM], old[2] = {0, 0};
+        f32x4 t[4] = {};
+        auto set_factors = [&](const Front &x, int n) {
+            const float sc = scale_b(n);
 #pragma unroll
-        for (int s = 0; s < S; ++s) static_for<L>([&](auto q) { load<decltype(q)::value>(s * kSlot, block(s)); });
-        s_wait_vm<(S - 1) * L>();
-        __builtin_amdgcn_s_barrier();
-        __builtin_amdgcn_sched_barrier(0);
-        i32x8 a[kRing], b[WN];
-        float f[WM];
-        f32x4 t[4];
-        auto scales = [&](int at, float (&o)[WM]) {
-#pragma unroll
-            for (int i = 0; i < WM; ++i) o[i] = *(const float *)(lds + at + rd_s + 4 * i);
+            for (int i = 0; i < WM; ++i) f[i] = x.raw[i] * sc;
         };
-        float raw[WM];
-        scales(0, raw);
-#pragma unroll
-        for (int j = 0; j < WN; ++j) b[j] = frag(0, rd_b, 2048 * j);
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) a[i] = frag(0, rd_a, 2048 * i);
-        const float s0 = scale_b(0);
-#pragma unroll
-        for (int i = 0; i < WM; ++i) f[i] = raw[i] * s0;
-        int at = 0;
-        for (int n = 0; n < count; ++n) {
-            const int next = at == (S - 1) * kSlot ? 0 : at + kSlot;
-            if ((n & 63) == 63) {
-                sbv = kb0 + n + 1 + lane < sbn ? sb[kb0 + n + 1 + lane] : 0.0f;
+        auto refill_scales = [&](int n) {
+            if ((n & 63) == 0) {
+                sbv = n + lane < nsb ? sb[n + lane] : 0.0f;
                 s_wait_vm<0>();
             }
-            const int fill = block(n + S);
-            static_for<WM * WN>([&](auto mm) {
-                constexpr int m = decltype(mm)::value, i = m / WN, j = m % WN;
-                if constexpr (i == WM - kAhead && j == 0) {
-                    s_wait_lgkm0();
-                    s_wait_vm<(S - 2) * L>();
-                    __builtin_amdgcn_s_barrier();
+        };
+        // the m-th MFMA, of b[j] and a[i], and the addition of an earlier one
+        auto mfma = [&](auto mm, const i32x8 &b, const i32x8 &a) {
+            constexpr int m = decltype(mm)::value;
+            t[m % 4] = mfma128<AE5>(b, a);
+            asm volatile("" : "+v"(t[m % 4]));      // (stays here, in the order written)
+            if constexpr (m >= 3) add<m - 3>(acc, f[(m - 3) / WN], t);
+            else add<N - 3 + m>(acc, old[WM - 1 - (N - 3 + m) / WN], t);
+        };
+        auto barrier = [&] {
+            // this block's fragments are in registers, the next block has landed
+            s_wait_lgkm0();
+            s_wait_vm<(S - 2) * L>();
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        auto keep_factors = [&] {
+            old[0] = f[WM - 1];
+            old[1] = f[WM - 2];
+        };
+        if constexpr (WHOLE) {
+            Front other;
+            auto step = [&](Front &cur, Front &nxt, int n) {
+                const int to = at == (S - 1) * kSlot ? 0 : at + kSlot;
+                // the slot's next block, this tile's or the next one's
+                const int fill = n + S < count ? n + S : n + S - count;
+                if (fill == 0) src = next;
+                set_factors(cur, n);
+                barrier();
+                constexpr int R = 1 + WN + WM, span = N * 3 / 4;
+                static_for<N>([&](auto mm) {
+                    constexpr int m = decltype(mm)::value, i = m / WN, j = m % WN;
+                    mfma(mm, cur.b[j], cur.a[i]);
+                    if constexpr (m < span)
+                        static_for<R * (m + 1) / span - R * m / span>([&](auto rr) {
+                            constexpr int q = R * m / span + decltype(rr)::value;
+                            if constexpr (q == 0) scales(to, nxt.raw);
+                            else if constexpr (q <= WN) nxt.b[q - 1] = frag(to, rd_b, 2048 * (q - 1));
+                            else nxt.a[q - 1 - WN] = frag(to, rd_a, 2048 * (q - 1 - WN));
+                        });
+                    static_for<L * (m + 1) / N - L * m / N>([&](auto q) { load<L * m / N + decltype(q)::value>(src, at, fill); });
                     __builtin_amdgcn_sched_barrier(0);
-                }
-                t[m % 4] = mfma128<AE5>(b[j], a[i % kRing]);
-                if constexpr (m >= 3) add<m - 3>(acc, f, t);
-                // the fragment kAhead rows on, this block's or the next one's
-                if constexpr (j == 0) {
-                    constexpr int o = i + kAhead;
-                    if constexpr (o < WM) a[o % kRing] = frag(at, rd_a, 2048 * o);
-                    else a[o % kRing] = frag(next, rd_a, 2048 * (o - WM));
-                }
-                if constexpr (i == WM - kAhead && j == 1 % WN) scales(next, raw);
-                if constexpr (i == WM - 1) b[j] = frag(next, rd_b, 2048 * j);
-                // refill the slot
-                constexpr int c = m - (WM - kAhead) * WN, slots = kAhead * WN;
-                if constexpr (c >= 0) {
-                    static_for<(L * (c + 1)) / slots - (L * c) / slots>([&](auto q) { load<(L * c) / slots + decltype(q)::value>(at, fill); });
-                }
-                __builtin_amdgcn_sched_barrier(0);
-            });
-            add<WM * WN - 3>(acc, f, t);
-            add<WM * WN - 2>(acc, f, t);
-            add<WM * WN - 1>(acc, f, t);
-            const float sc = scale_b(n + 1);
-#pragma unroll
-            for (int i = 0; i < WM; ++i) f[i] = raw[i] * sc;
-            at = next;
+                });
+                keep_factors();
+                at = to;
+            };
+            for (int n = 0; n < count; n += 2) {
+                if (n) refill_scales(n);
+                step(fr, other, n);
+                step(other, fr, n + 1);
+            }
+        } else {
+            set_factors(fr, 0);
+            for (int n = 0; n < count; ++n) {
+                const int to = at == (S - 1) * kSlot ? 0 : at + kSlot;
+                refill_scales(n + 1);
+                const int fill = n + S < count ? n + S : n + S - count;
+                if (fill == 0) src = next;
+                static_for<N>([&](auto mm) {
+                    constexpr int m = decltype(mm)::value, i = m / WN, j = m % WN;
+                    if constexpr (i == WM - kAhead && j == 0) barrier();
+                    mfma(mm, fr.b[j], fr.a[i % kRing]);
+                    // the fragment kAhead rows on, this block's or the next one's
+                    if constexpr (j == 0) {
+                        constexpr int o = i + kAhead;
+                        if constexpr (o < WM) fr.a[o % kRing] = frag(at, rd_a, 2048 * o);
+                        else fr.a[o % kRing] = frag(to, rd_a, 2048 * (o - WM));
+                    }
+                    if constexpr (i == WM - kAhead && j == 1 % WN) scales(to, fr.raw);
+                    if constexpr (i == WM - 1) fr.b[j] = frag(to, rd_b, 2048 * j);
+                    // refill the slot
+                    constexpr int c = m - (WM - kAhead) * WN, slots = kAhead * WN;
+                    if constexpr (c >= 0) {
+                        static_for<(L * (c + 1)) / slots - (L * c) / slots>([&](auto q) {
+                            load<(L * c) / slots + decltype(q)::value>(src, at, fill);
+                        });
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                });
+                keep_factors();
+                set_factors(fr, n + 1);
+                at = to;
+            }
         }
-        s_wait_vm<0>();
-        s_wait_lgkm0();
-        __builtin_amdgcn_s_barrier();       // the ring is free: the epilogue stages in it
-        __builtin_amdgcn_sched_barrier(0);
+        static_for<3>([&](auto mm) {
+            constexpr int m = N - 3 + decltype(mm)::value;
+            add<m>(acc, old[WM - 1 - m / WN], t);
+        });
+    }
+
+    // acc to C, 16 rows at a time through LDS of its own, so that whole lines are
+    // stored.
+    template <int CT>
+    __device__ __forceinline__ void store(const Place &p, int64_t ldc, const f32x4 (&acc)[WM][WN]) const
+    {
+        uint8_t *const reg = lds + S * kSlot + w * kStage;
+        const int r0 = 16 * WM * wm, c0 = 16 * WN * wn;
+        constexpr int LPR = RB / 16, RPI = 64 / LPR;            // lanes a row, rows a store
+        const int lr = lane / LPR, cb = lane % LPR * 16;
+        const uint32_t row_bytes = (uint32_t)(2 * ldc);
+        const uint64_t base = (uint64_t)(uintptr_t)(p.c + 2 * (r0 * ldc + c0));
+        const int rows = max(0, min(p.rows - r0, 16 * WM));
+        void *const dst = (void *)(uintptr_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(base >> 32)) << 32) |
+                                              (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)base));
+        const uint32_t n = (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)rows * row_bytes));
+        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(dst, (short)0, (int)n, 0x00020000);
+        const uint32_t voff = cb < 2 * (p.cols - c0) ? (uint32_t)lr * row_bytes + (uint32_t)cb : kOOB;
+        // whole 128-byte lines go past the L2, which is left to the operands
+        constexpr int kNT = RB % 128 == 0 ? 2 : 0;
+        static_for<WM>([&](auto ii) {
+            constexpr int i = decltype(ii)::value;
+            __builtin_amdgcn_sched_barrier(0);
+            static_for<WN>([&](auto jj) {
+                const f32x4 x = acc[i][decltype(jj)::value];
+                *(uint2 *)(reg + (lane & 15) * kRow + 8 * (lane >> 4) + 32 * decltype(jj)::value) = pack_quad<CT>(x[0], x[1], x[2], x[3]);
+            });
+#pragma unroll
+            for (int k = 0; k < 16 / RPI; ++k) {
+                const i32x4 v = *(const i32x4 *)(reg + (lr + k * RPI) * kRow + cb);
+                __builtin_amdgcn_raw_buffer_store_b128(v, rs, voff + (uint32_t)(16 * i + k * RPI) * row_bytes, 0, kNT);
+            }
+        });
+    }
+
+    // acc to a part's sums (fp32).
+    __device__ __forceinline__ void put_sums(const Place &p, int64_t ldc, const f32x4 (&acc)[WM][WN]) const
+    {
+        static_for<WM>([&](auto ii) {
+            const int r = 16 * (WM * wm + decltype(ii)::value) + (lane & 15);
+            static_for<WN>([&](auto jj) {
+                const int c = 16 * (WN * wn + decltype(jj)::value) + 4 * (lane >> 4);
+                if (r < p.rows && c < p.cols) *(f32x4 *)((float *)p.c + r * ldc + c) = acc[decltype(ii)::value][decltype(jj)::value];
+            });
+        });
     }
 
 private:
     template <int M>
-    static __device__ __forceinline__ void add(f32x4 (&acc)[WM][WN], const float (&f)[WM], const f32x4 (&t)[4])
+    static __device__ __forceinline__ void add(f32x4 (&acc)[WM][WN], float f, const f32x4 (&t)[4])
     {
 #pragma unroll
-        for (int v = 0; v < 4; ++v) acc[M / WN][M % WN][v] = fmaf(f[M / WN], t[M % 4][v], acc[M / WN][M % WN][v]);
+        for (int v = 0; v < 4; ++v) acc[M / WN][M % WN][v] = fmaf(f, t[M % 4][v], acc[M / WN][M % WN][v]);
     }
 };
 

@@ -643,7 +643,7 @@ int gemm_fp8(const uint8_t *a, const uint8_t *b, const float *a_scale, const flo
  *   (num_experts, ceil(n/128), ceil(k/128)).  Also the input's gradient, with
  *   the transposed codes of the weights.
  *   expert_rows (num_experts,) or NULL: the rows of a range from there on are
- *   not read and give zeros (NULL: every row of a range counts).
+ *   neither read nor written (NULL: every row of a range counts).
  *   max_rows: no expert has more rows than this, as the caller knows from its
  *   number of tokens; 0 if it does not.  It chooses the kernel only (few rows:
  *   one that is bound by the weights' bytes; it needs expert_rows); any value

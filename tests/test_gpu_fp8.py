@@ -136,7 +136,7 @@ def test_grouped_gemm_fp8(counts, m, n, k, kind):
             last, end = at + (counts[e] if use_rows else int(ends[e]) - at), int(ends[e])
             if last > at:
                 compare(c[at:last], a[at:last], x, sa[:, at:last], s, kind, dt, f"expert {e}")
-            assert bool((c[last:end] == 0).all())
+            assert bool((c[last:end] == 5).all())       # rows that hold no pair stay as they are
             at = end
         assert bool((c[at:] == 5).all())
 
