@@ -162,8 +162,8 @@ struct Fp8Tile {
         float raw[WM];
     };
 
-    // The first S blocks of the first tile, and its front.
-    __device__ __forceinline__ void start(const Source &s, Front &f)
+    // The first S blocks of the first tile.
+    __device__ __forceinline__ void start(const Source &s) const
     {
         static_for<S>([&](auto n) {
             static_for<L>([&](auto q) { load<decltype(q)::value>(s, decltype(n)::value * kSlot, decltype(n)::value); });
@@ -171,11 +171,6 @@ struct Fp8Tile {
         s_wait_vm<(S - 1) * L>();
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        scales(0, f.raw);
-#pragma unroll
-        for (int j = 0; j < WN; ++j) f.b[j] = frag(0, rd_b, 2048 * j);
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) f.a[i] = frag(0, rd_a, 2048 * i);
     }
 
     // Blocks that run() is called for: whole steps, and as many as the ring has
@@ -185,11 +180,11 @@ struct Fp8Tile {
         return max(WHOLE ? (blocks + 1) & ~1 : blocks, kMin);
     }
 
-    // acc = sum over the `count` blocks of a tile; leaves the front of the next
-    // tile's first block, whose loads come from `next`.  sb: B's scales of the
-    // wave's columns, nsb of them.
+    // acc = sum over the `count` blocks of a tile, the first of which has landed,
+    // as has that of the next tile, whose loads come from `next`, in the end.  sb:
+    // B's scales of the wave's columns, nsb of them.
     template <bool AE5>
-    __device__ __forceinline__ void run(f32x4 (&acc)[WM][WN], Front &fr, Source src, const Source &next, int count,
+    __device__ __forceinline__ void run(f32x4 (&acc)[WM][WN], Source src, const Source &next, int count,
                                         const float *sb, int nsb)
     {
         // B's scales of 64 blocks, one a lane
@@ -233,6 +228,12 @@ struct Fp8Tile {
             old[0] = f[WM - 1];
             old[1] = f[WM - 2];
         };
+        Front fr;
+        scales(at, fr.raw);
+#pragma unroll
+        for (int j = 0; j < WN; ++j) fr.b[j] = frag(at, rd_b, 2048 * j);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) fr.a[i] = frag(at, rd_a, 2048 * i);
         if constexpr (WHOLE) {
             Front other;
             auto step = [&](Front &cur, Front &nxt, int n) {
@@ -303,6 +304,20 @@ struct Fp8Tile {
         });
     }
 
+    // run() of a wave whose rows lie behind the tile's last one: its share of the
+    // loads, and the barriers.  The waves that have rows then have the matrix
+    // cores to themselves.
+    __device__ __forceinline__ void run_idle(Source src, const Source &next, int count)
+    {
+        for (int n = 0; n < count; ++n) {
+            s_wait_vm<(S - 2) * L>();
+            __builtin_amdgcn_s_barrier();
+            const int fill = n + S < count ? n + S : n + S - count;
+            if (fill == 0) src = next;
+            static_for<L>([&](auto q) { load<decltype(q)::value>(src, at, fill); });
+            at = at == (S - 1) * kSlot ? 0 : at + kSlot;
+        }
+    }
     // acc to C, 16 rows at a time through LDS of its own, so that whole lines are
     // stored.
     template <int CT>

@@ -58,63 +58,179 @@ __device__ __forceinline__ Part part_of(const Fp8Args &p, int64_t m0, int tm, in
             {c, sb, rows, cols}};
 }
 
-// Workgroup b takes the tiles b, b + gridDim.x, ... in the order of tile_at;
-// the loads of a tile's first blocks go out in the last blocks of the one
-// before it, so that only the way out of a tile keeps the matrix cores waiting.
-// With K in parts (gemm_fp8) a tile is a part of one, whose sums go to the
-// workspace.
-template <class T, bool AE5, int CT>
-__global__ __launch_bounds__(T::kThreads, T::kWaves) void k_fp8(Fp8Args p, unsigned mt, unsigned nt, int splits)
+// The tiles of one workgroup, in turn.
+//
+// Big tiles that a last round of at most half the compute units would take go
+// out in halves of 128 rows, to twice as many workgroups: a half, whose other
+// waves are idle, takes 0.6 of a whole one's time.
+template <class T>
+struct Stride {
+    const Fp8Args &p;
+    unsigned mt, nt, total, whole, units, next;
+    __device__ __forceinline__ Stride(const Fp8Args &p, unsigned mt, unsigned nt, unsigned splits) : p(p), mt(mt), nt(nt), next(blockIdx.x)
+    {
+        total = mt * nt * splits;
+        whole = total / gridDim.x * gridDim.x;
+        const unsigned rest = total - whole;
+        if (T::TM < 256 || 2 * rest > gridDim.x) whole = total;
+        units = whole + 2 * (total - whole);
+    }
+    // the next tile that has rows; false behind the last one
+    __device__ __forceinline__ bool take(Part &t)
+    {
+        for (; next < units; next += gridDim.x) {
+            unsigned i = next;
+            int half = 0;
+            if (i >= whole) {
+                const unsigned j = i - whole, rest = total - whole;
+                half = j >= rest;
+                i = whole + (half ? j - rest : j);
+            }
+            const ffn::TileAt at = ffn::tile_at(i, mt, nt);
+            t = part_of(p, (int64_t)T::TM * at.m + T::TM / 2 * half, next < whole ? T::TM : T::TM / 2, (int64_t)T::TN * at.n, T::TN, 0);
+            if (t.to.rows > 0) break;
+        }
+        const bool some = next < units;
+        next += gridDim.x;
+        return some;
+    }
+};
+
+// A part of K of a tile each (gemm_fp8).
+template <class T>
+struct Parts {
+    const Fp8Args &p;
+    unsigned mt, nt, splits, next;
+    __device__ __forceinline__ Parts(const Fp8Args &p, unsigned mt, unsigned nt, unsigned splits)
+        : p(p), mt(mt), nt(nt), splits(splits), next(blockIdx.x)
+    {
+    }
+    __device__ __forceinline__ bool take(Part &t)
+    {
+        if (next >= mt * nt * splits) return false;
+        const auto [at, split] = ffn::split_tile(next, mt, nt, splits);
+        const ffn::Split s = ffn::split_of(split, (int)splits, (int)((p.k + 127) / 128));
+        const int64_t first = 128ll * s.first, m0 = (int64_t)T::TM * at.m, n0 = (int64_t)T::TN * at.n;
+        t = part_of(p, m0, T::TM, n0, T::TN, 0);
+        // (the bytes of the rows shrink by what their beginning moves)
+        t.src.ra = make_rsrc_words(p.a + m0 * p.k + first, ffn::clamp_bytes(t.to.rows * p.k - first));
+        t.src.rb = make_rsrc_words(p.b + n0 * p.k + first, ffn::clamp_bytes(t.to.cols * p.k - first));
+        t.src.sa += s.first * p.m;
+        t.src.klimit = (uint32_t)min(p.k - first, 128ll * s.count);
+        t.to.sb += s.first;
+        t.to.c = (char *)((float *)p.workspace + (s.index * p.m + m0) * p.n + n0);
+        next += gridDim.x;
+        return true;
+    }
+};
+
+// GROUP_K: experts differ in how long their sums are, so the tiles of all of
+// them, expert by expert, are cut into a run of equal work for each XCD (a
+// tile's way out counts as kOut blocks), and the XCD's workgroups take its run's
+// tiles in turn: at any time they share an expert's operands in their L2, and
+// each has as many tiles of every expert as the others.
+template <class T>
+struct Runs {
+    static constexpr int kOut = 4;
+    const Fp8Args &p;
+    unsigned mt, nt, per, step;
+    int e, w;                       // the next tile's expert, and the work of each of its tiles
+    unsigned index;                 // the next tile of the expert's `per`
+    uint64_t begins, end;           // where the expert begins in all the work, and the run ends
+    __device__ __forceinline__ int work(int i) const
+    {
+        if (i >= p.num_experts) return 0;
+        const int64_t first = i ? p.padded_offsets[i - 1] : 0, last = min((int64_t)p.padded_offsets[i], p.k);
+        return (int)(max((int64_t)0, last - first) / 128) + kOut;
+    }
+    __device__ __forceinline__ Runs(const Fp8Args &p, unsigned mt, unsigned nt, unsigned) : p(p), mt(mt), nt(nt), per(mt * nt)
+    {
+        const int lane = threadIdx.x & 63;
+        auto scan = [&](int x) {        // sums up to and with this lane
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2) {
+                const int o = __shfl_up(x, d);
+                x += lane >= d ? o : 0;
+            }
+            return x;
+        };
+        uint64_t all = 0;
+        for (int i = 0; i < p.num_experts; i += 64) all += (uint32_t)__builtin_amdgcn_readlane(scan(work(i + lane)), 63);
+        all *= per;
+        const unsigned runs = gridDim.x % 8 ? 1 : 8, run = blockIdx.x % runs;
+        step = gridDim.x / runs;
+        const uint64_t at = all * run / runs;
+        end = all * (run + 1) / runs;
+        // the first tile that begins at or behind the run's beginning
+        e = p.num_experts;
+        w = 1;
+        index = 0;
+        begins = 0;
+        uint64_t before = 0;
+        for (int i = 0; i < p.num_experts; i += 64) {
+            const int x = work(i + lane), s = scan(x);
+            const uint64_t ends = before + (uint64_t)s * per;
+            const uint64_t found = __ballot(i + lane < p.num_experts && ends > at);
+            if (found) {
+                const int l = __builtin_ctzll(found);
+                e = i + l;
+                w = __builtin_amdgcn_readlane(x, l);
+                begins = before + (uint64_t)(uint32_t)(__builtin_amdgcn_readlane(s, l) - w) * per;
+                index = at > begins ? (unsigned)((at - begins + w - 1) / w) : 0;
+                break;
+            }
+            before += (uint64_t)(uint32_t)__builtin_amdgcn_readlane(s, 63) * per;
+        }
+        index += blockIdx.x / runs;
+    }
+    __device__ __forceinline__ bool take(Part &t)
+    {
+        while (index >= per && e < p.num_experts) {
+            index -= per;
+            begins += (uint64_t)(uint32_t)w * per;
+            w = uniform(work(++e));
+        }
+        if (e >= p.num_experts || begins + (uint64_t)(uint32_t)w * index >= end) return false;
+        // strips of four rows of tiles, column by column
+        const unsigned strip = index / (4 * nt), r = index % (4 * nt), rows = min(4u, mt - 4 * strip);
+        t = part_of(p, (int64_t)T::TM * (4 * strip + r % rows), T::TM, (int64_t)T::TN * (r / rows), T::TN, e);
+        index += step;
+        return true;
+    }
+};
+
+// A workgroup goes from tile to tile; the loads of a tile's first blocks go out
+// in the last blocks of the one before it, so that only the way out of a tile
+// keeps the matrix cores waiting.
+template <class T, template <class> class Walk, bool AE5, int CT>
+__global__ __launch_bounds__(T::kThreads, T::kWaves) void k_fp8(Fp8Args p, unsigned mt, unsigned nt, unsigned splits)
 {
-    constexpr bool SPLIT = T::SUMS;
     __shared__ __attribute__((aligned(16))) uint8_t ring[T::kLds];
     // rows behind the last expert are no tiles
     if (p.group == GROUP_ROWS)
         mt = (unsigned)((min((int64_t)max(p.padded_offsets[p.num_experts - 1], 0), p.m) + T::TM - 1) / T::TM);
-    const unsigned rows = p.group == GROUP_K ? mt * p.num_experts : mt, total = rows * nt * (SPLIT ? splits : 1);
-    auto part = [&](unsigned i) {
-        const auto [at, split] = ffn::tile_of_block<SPLIT>(i, rows, nt, splits);
-        const int z = p.group == GROUP_K ? at.m / (int)mt : 0;
-        Part t = part_of(p, (int64_t)T::TM * (at.m - z * (int)mt), T::TM, (int64_t)T::TN * at.n, T::TN, z);
-        if constexpr (SPLIT) {
-            const ffn::Split s = ffn::split_of(split, splits, (int)((p.k + 127) / 128));
-            const int64_t first = 128ll * s.first;
-            // (the bytes of the rows shrink by what their beginning moves)
-            t.src.ra = make_rsrc_words(p.a + (int64_t)T::TM * at.m * p.k + first, ffn::clamp_bytes(t.to.rows * p.k - first));
-            t.src.rb = make_rsrc_words(p.b + (int64_t)T::TN * at.n * p.k + first, ffn::clamp_bytes(t.to.cols * p.k - first));
-            t.src.sa += s.first * p.m;
-            t.src.klimit = (uint32_t)min(p.k - first, 128ll * s.count);
-            t.to.sb += s.first;
-            t.to.c = (char *)((float *)p.workspace + (s.index * p.m + (int64_t)T::TM * at.m) * p.n + (int64_t)T::TN * at.n);
-        }
-        return t;
-    };
-    // the next tile with rows from i on, or one past them all
+    Walk<T> walk(p, mt, nt, splits);
     Part cur;
-    auto seek = [&](unsigned i, Part &t) {
-        for (; i < total; i += gridDim.x) {
-            t = part(i);
-            if (t.to.rows > 0) break;
-        }
-        return i;
-    };
-    unsigned b = seek(blockIdx.x, cur);
-    if (b >= total) return;
+    if (!walk.take(cur)) return;
     T tile(ring, p.k, p.m);
-    typename T::Front front;
-    tile.start(cur.src, front);
-    for (;;) {
+    tile.start(cur.src);
+    bool more = true;
+    while (more) {
         Part then = cur;
-        b = seek(b + gridDim.x, then);
-        if (b >= total) then.src.klimit = 0;            // nothing after the last tile
-        f32x4 acc[T::WM][T::WN];
-        const int blocks = (int)((cur.src.klimit + 127) / 128);
-        tile.template run<AE5>(acc, front, cur.src, then.src, T::count_of(blocks),
-                               cur.to.sb + 16 * T::WN * tile.wn / 128 * ((p.k + 127) / 128), blocks);
-        if (b >= total) s_wait_vm<0>();         // no load is under way to the LDS when the workgroup ends
-        if constexpr (SPLIT) tile.put_sums(cur.to, p.n, acc);
-        else tile.template store<CT>(cur.to, p.n, acc);
-        if (b >= total) break;
+        more = walk.take(then);
+        if (!more) then.src.klimit = 0;         // nothing after the last tile
+        const int blocks = (int)((cur.src.klimit + 127) / 128), count = T::count_of(blocks);
+        if (cur.to.rows <= 16 * T::WM * tile.wm) {
+            tile.run_idle(cur.src, then.src, count);
+            if (!more) s_wait_vm<0>();
+        } else {
+            f32x4 acc[T::WM][T::WN];
+            tile.template run<AE5>(acc, cur.src, then.src, count, cur.to.sb + 16 * T::WN * tile.wn / 128 * ((p.k + 127) / 128),
+                                   blocks);
+            if (!more) s_wait_vm<0>();          // no load is under way to the LDS when the workgroup ends
+            if constexpr (T::SUMS) tile.put_sums(cur.to, p.n, acc);
+            else tile.template store<CT>(cur.to, p.n, acc);
+        }
         cur = then;
     }
 }
@@ -257,12 +373,21 @@ typedef Fp8Tile<8, 4, 2, 4, 2> Big;         // 256 x 256, 8 waves
 typedef Fp8Tile<4, 4, 2, 2, 2> Mid;         // 128 x 128, 4 waves, two workgroups a compute unit
 typedef Fp8Tile<2, 2, 2, 4, 3> Small;       // 64 x 128, 8 waves, with K in parts two workgroups a compute unit
 
-template <class T, bool AE5, int CT>
+template <class T, template <class> class Walk, bool AE5, int CT>
 void go_tiles(const Fp8Args &a, int splits, hipStream_t s)
 {
-    const unsigned mt = (unsigned)((a.m + T::TM - 1) / T::TM), nt = (unsigned)((a.n + T::TN - 1) / T::TN);
-    const unsigned tiles = mt * nt * (a.group == GROUP_K ? a.num_experts : 1) * splits;
-    k_fp8<T, AE5, CT><<<min(tiles, 256u * T::kGroups), T::kThreads, 0, s>>>(a, mt, nt, splits);
+    const int64_t mt = (a.m + T::TM - 1) / T::TM, nt = (a.n + T::TN - 1) / T::TN;
+    // (Big ones may go out in halves)
+    const int64_t tiles = mt * nt * (a.group == GROUP_K ? a.num_experts : 1) * splits * (T::TM / 128 > 1 ? 2 : 1);
+    k_fp8<T, Walk, AE5, CT><<<(unsigned)std::min(tiles, (int64_t)256 * T::kGroups), T::kThreads, 0, s>>>(a, (unsigned)mt, (unsigned)nt,
+                                                                                                      (unsigned)splits);
+}
+
+template <class T, bool AE5, int CT>
+void go_whole(const Fp8Args &a, hipStream_t s)
+{
+    if (a.group == GROUP_K) go_tiles<T, Runs, AE5, CT>(a, 1, s);
+    else go_tiles<T, Stride, AE5, CT>(a, 1, s);
 }
 
 template <bool AE5, int CT>
@@ -272,14 +397,14 @@ void launch(const Fp8Args &a, const Plan &p, hipStream_t s)
     if (p.few == 32) return go_few<AE5, CT, 2>(a, s);
     if (p.few == 64) return go_few<AE5, CT, 4>(a, s);
     if (p.splits > 1) {
-        go_tiles<Small::Sums, AE5, CT>(a, p.splits, s);
+        go_tiles<Small::Sums, Parts, AE5, CT>(a, p.splits, s);
         k_join<CT><<<(unsigned)((a.m * a.n / 4 + 255) / 256), 256, 0, s>>>(a, p.splits);
     } else if (p.shape == BIG) {
-        go_tiles<Big, AE5, CT>(a, 1, s);
+        go_whole<Big, AE5, CT>(a, s);
     } else if (p.shape == MID) {
-        go_tiles<Mid, AE5, CT>(a, 1, s);
+        go_whole<Mid, AE5, CT>(a, s);
     } else {
-        go_tiles<Small, AE5, CT>(a, 1, s);
+        go_tiles<Small, Stride, AE5, CT>(a, 1, s);
     }
 }
 
