@@ -80,6 +80,9 @@ struct Fp8Tile {
     // one block's columns and kRing of its rows, where two do not fit.
     static constexpr bool WHOLE = WM < 4;
     static constexpr int kRing = WHOLE ? WM : 4, kAhead = WHOLE ? WM : 3;
+    // B's share of a slot is free, and filled again, when its columns are in
+    // registers, a block's length before A's
+    static constexpr bool EARLY = WM >= 8;
     static constexpr int kMin = WHOLE ? (S + 1) / 2 * 2 : S;                    // least blocks of a tile
     static constexpr int N = WM * WN;
     static_assert(128 % (16 * WN) == 0, "a wave's columns lie in one 128");
@@ -220,7 +223,7 @@ struct Fp8Tile {
         auto barrier = [&] {
             // this block's fragments are in registers, the next block has landed
             s_wait_lgkm0();
-            s_wait_vm<(S - 2) * L>();
+            s_wait_vm<(S - 2) * L + (EARLY ? LB : 0)>();
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_sched_barrier(0);
         };
@@ -274,6 +277,11 @@ struct Fp8Tile {
                 if (fill == 0) src = next;
                 static_for<N>([&](auto mm) {
                     constexpr int m = decltype(mm)::value, i = m / WN, j = m % WN;
+                    // every wave has this block's columns in registers
+                    if constexpr (EARLY && i == 1 && j == 0) {
+                        __builtin_amdgcn_s_barrier();
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
                     if constexpr (i == WM - kAhead && j == 0) barrier();
                     mfma(mm, fr.b[j], fr.a[i % kRing]);
                     // the fragment kAhead rows on, this block's or the next one's
@@ -284,13 +292,21 @@ struct Fp8Tile {
                     }
                     if constexpr (i == WM - kAhead && j == 1 % WN) scales(to, fr.raw);
                     if constexpr (i == WM - 1) fr.b[j] = frag(to, rd_b, 2048 * j);
-                    // refill the slot
-                    constexpr int c = m - (WM - kAhead) * WN, slots = kAhead * WN;
-                    if constexpr (c >= 0) {
+                    // refill the slot: columns, then rows
+                    constexpr int c = m - (WM - kAhead) * WN, slots = kAhead * WN, early = m - WN, room = (WM - kAhead - 1) * WN;
+                    if constexpr (EARLY && early >= 0 && early < room)
+                        static_for<(LB * (early + 1)) / room - (LB * early) / room>([&](auto q) {
+                            load<LA + (LB * early) / room + decltype(q)::value>(src, at, fill);
+                        });
+                    if constexpr (!EARLY && c >= 0)
                         static_for<(L * (c + 1)) / slots - (L * c) / slots>([&](auto q) {
                             load<(L * c) / slots + decltype(q)::value>(src, at, fill);
                         });
-                    }
+                    if constexpr (EARLY && c >= 0)
+                        static_for<((LA + 1) * (c + 1)) / slots - ((LA + 1) * c) / slots>([&](auto q) {
+                            constexpr int x = ((LA + 1) * c) / slots + decltype(q)::value;
+                            load<(x < LA ? x : LA + LB)>(src, at, fill);
+                        });
                     __builtin_amdgcn_sched_barrier(0);
                 });
                 keep_factors();
@@ -310,11 +326,17 @@ struct Fp8Tile {
     __device__ __forceinline__ void run_idle(Source src, const Source &next, int count)
     {
         for (int n = 0; n < count; ++n) {
-            s_wait_vm<(S - 2) * L>();
-            __builtin_amdgcn_s_barrier();
             const int fill = n + S < count ? n + S : n + S - count;
             if (fill == 0) src = next;
-            static_for<L>([&](auto q) { load<decltype(q)::value>(src, at, fill); });
+            if constexpr (EARLY) {
+                __builtin_amdgcn_s_barrier();
+                static_for<LB>([&](auto q) { load<LA + decltype(q)::value>(src, at, fill); });
+            }
+            s_wait_vm<(S - 2) * L + (EARLY ? LB : 0)>();
+            __builtin_amdgcn_s_barrier();
+            static_for<LA>([&](auto q) { load<decltype(q)::value>(src, at, fill); });
+            if constexpr (!EARLY) static_for<LB>([&](auto q) { load<LA + decltype(q)::value>(src, at, fill); });
+            load<LA + LB>(src, at, fill);
             at = at == (S - 1) * kSlot ? 0 : at + kSlot;
         }
     }
