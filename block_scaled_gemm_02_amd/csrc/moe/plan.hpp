@@ -78,16 +78,26 @@ inline Plan plan_gemm_fp8(int64_t m, int64_t n, int64_t k)
 // grouped_gemm_fp8.  The host knows the rows that the buffer has and the most
 // that one expert may have, not how many there are.  If m is what bsg_moe_rows
 // gives, there are at most m + 255 - 255 num_experts pairs, so that many over
-// the experts on average.  Up to 8 rows an expert the few-row kernel reads the
-// weights faster, past that its workgroups read the rows too often (us, few /
-// tiles: 64 experts of 4096 x 7168 with 4 rows each 339 / 390, with 16 rows 509 /
-// 391; 8 experts with 8 rows 44.6 / 50.7, with one row 38 / 51).
+// the experts on average.  Tiles of at most 64 rows each read the experts'
+// weights at 5.9 (Big) or 4.6 TB/s (Mid), the few-row kernel at 5.5, and its
+// workgroups the rows again (us, few / Big / Mid: 64 experts of 4096 x 7168 with
+// 4 rows each 339 / 318 / 497, with 16 rows 509 / 325 / 502; 8 experts with 8
+// rows 44.6 / 69 / 51, with one row 38 / 69 / 51).
 inline Plan plan_grouped_fp8(int64_t m, int64_t n, int64_t k, int64_t num_experts, int64_t max_rows, bool expert_rows)
 {
-    const int64_t pairs = m + 255 - 255 * num_experts;
-    if (expert_rows && max_rows > 0 && max_rows <= 64 && pairs <= 8 * num_experts) return {max_rows <= 16 ? 16 : 32, BIG, 1, 0};
     const Plan big = plan_with(BIG, 1, m, n, k, 1), mid = plan_with(MID, 1, m, n, k, 1);
-    return mid.us < big.us ? mid : big;
+    Plan best = mid.us < big.us ? mid : big;
+    if (expert_rows && max_rows > 0 && max_rows <= 64) {
+        const int64_t blocks = m / 256, experts = std::min(num_experts, blocks), pairs = m + 255 - 255 * num_experts;
+        const double each = std::max(1.0, (double)pairs / (double)num_experts), bytes = (double)experts * (double)n * (double)k;
+        const int64_t tiles = blocks * ((n + 255) / 256);
+        const double tb = std::max((double)((tiles + 255) / 256) * (5.2 + 1.15 * (double)ffn::pairs_in(k)) + 1.8, 3.5 + bytes / 5.9e6);
+        const double tm = std::max(plan_with(MID, 1, 128 * blocks, n, k, 1).us, 3.5 + bytes / 4.6e6);
+        const double tf = 2.5 + bytes / 5.5e6 + (double)experts * (double)n / 4096 * std::max(0.0, each - 6) * (double)k / 45000;
+        best = {0, tm < tb ? MID : BIG, 1, std::min(tm, tb)};
+        if (tf < best.us) best = {max_rows <= 16 ? 16 : 32, BIG, 1, tf};
+    }
+    return best;
 }
 
 // grouped_gemm_fp8_wgrad: C (n, k) for each expert, its rows m over the experts.
