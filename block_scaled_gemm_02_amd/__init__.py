@@ -159,7 +159,8 @@ def _need(t, name, nbytes, kind=None):
     if not t.is_contiguous():
         raise BsgError(4, f"{name} must be contiguous")
     if isinstance(kind, torch.dtype):
-        if t.dtype != kind:
+        # 8-bit floats may come as plain bytes
+        if t.dtype != kind and not (t.dtype == torch.uint8 and kind in (torch.float8_e4m3fn, torch.float8_e5m2)):
             raise BsgError(3, f"{name} must be {kind} (got {t.dtype})")
     elif kind in _OUT_TORCH:
         if t.dtype != _OUT_TORCH[kind]:
@@ -603,17 +604,16 @@ _I32 = torch.int32
 _FP8 = {"e4m3": (E4M3, torch.float8_e4m3fn), "e5m2": (E5M2, torch.float8_e5m2)}
 
 
+_E4M3 = torch.float8_e4m3fn
+_ES = {F32: 4, F16: 2, BF16: 2}       # bytes of an element (1 for what the call will refuse)
+
+
 def _fp8(fmt):
-    """The bsg_dtype code of an 8-bit float format's name."""
-    if fmt not in _FP8:
+    """The bsg_dtype code and torch dtype of an 8-bit float format's name."""
+    f = _FP8.get(fmt)
+    if f is None:
         raise ValueError(f"an 8-bit float format is one of {sorted(_FP8)}, got {fmt!r}")
-    return _FP8[fmt][0]
-
-
-def _codes_of(t, fmt):
-    """The dtype that a tensor of codes has to have: the format's own, or bytes."""
-    _fp8(fmt)
-    return torch.uint8 if isinstance(t, torch.Tensor) and t.dtype is torch.uint8 else _FP8[fmt][1]
+    return f
 
 
 def moe_rows(tokens, top_k, num_experts) -> int:
@@ -647,13 +647,18 @@ def moe_gather(x, row_of, padded_offsets, expert_rows, weight, y, scale, prob, t
     a float8_e4m3fn y) with scale (ceil(hidden / 128), m).  weight and prob may
     be None.  zero_pad: rows of an expert's range without a pair become zeros."""
     xd = _code(x_dtype, x)
-    yd = _d_code(y_dtype, y) if y_dtype is not None or isinstance(y, torch.Tensor) else xd
-    out = _codes_of(y, "e4m3") if yd == E4M3 else _TORCH_OF.get(yd)
+    if y_dtype is not None:
+        yd = _d_code(y_dtype, y)
+    elif isinstance(y, torch.Tensor):
+        yd = xd if y.dtype is _TORCH_OF.get(xd) else _d_code(None, y)
+    else:
+        yd = xd
+    out = _E4M3 if yd == E4M3 else _TORCH_OF.get(yd)
     pairs = 4 * tokens * top_k
-    args = _addresses((x, "x", _out_bytes(xd, tokens * hidden), _TORCH_OF.get(xd)), (row_of, "row_of", pairs, _I32),
+    args = _addresses((x, "x", _ES.get(xd, 1) * tokens * hidden, _TORCH_OF.get(xd)), (row_of, "row_of", pairs, _I32),
                       (padded_offsets, "padded_offsets", 4 * num_experts, _I32),
                       (expert_rows, "expert_rows", 4 * num_experts, _I32), (weight, "weight", pairs, _F32),
-                      (y, "y", _out_bytes(yd, m * hidden), out), (scale, "scale", 4 * m * _cdiv(hidden, 128), _F32),
+                      (y, "y", _ES.get(yd, 1) * m * hidden, out), (scale, "scale", 4 * m * -(-hidden // 128), _F32),
                       (prob, "prob", 4 * m, _F32))
     args += (tokens, hidden, top_k, num_experts, m, int(bool(zero_pad)), xd, yd)
     if validate_only:
@@ -666,10 +671,11 @@ def moe_gather_bwd(dy, dprob, row_of, dx, dweight, tokens, hidden, top_k, m, dty
     """Gradients of moe_gather: dx[t] = sum_j dy[row_of[t, j]] and dweight[t, j]
     = dprob[row_of[t, j]] (see include/bsg.h).  dprob and dweight, or dy and dx,
     may be None."""
-    dt = _code(dtype, dx if dtype is None and dx is not None else dy) if dx is not None or dy is not None or dtype is not None else F32
-    td, pairs = _TORCH_OF.get(dt), 4 * tokens * top_k
-    args = _addresses((dy, "dy", _out_bytes(dt, m * hidden), td), (dprob, "dprob", 4 * m, _F32),
-                      (row_of, "row_of", pairs, _I32), (dx, "dx", _out_bytes(dt, tokens * hidden), td),
+    like = dy if dx is None else dx
+    dt = F32 if dtype is None and like is None else _code(dtype, like)
+    td, pairs, es = _TORCH_OF.get(dt), 4 * tokens * top_k, _ES.get(dt, 1)
+    args = _addresses((dy, "dy", es * m * hidden, td), (dprob, "dprob", 4 * m, _F32),
+                      (row_of, "row_of", pairs, _I32), (dx, "dx", es * tokens * hidden, td),
                       (dweight, "dweight", pairs, _F32))
     args += (tokens, hidden, top_k, m, dt)
     if validate_only:
@@ -681,9 +687,9 @@ def moe_combine(y, row_of, weight, out, tokens, hidden, top_k, m, dtype=None, st
     """out[t] = sum_j weight[t, j] y[row_of[t, j]] (see include/bsg.h); weight
     None: ones."""
     dt = _code(dtype, out)
-    td, pairs = _TORCH_OF.get(dt), 4 * tokens * top_k
-    args = _addresses((y, "y", _out_bytes(dt, m * hidden), td), (row_of, "row_of", pairs, _I32),
-                      (weight, "weight", pairs, _F32), (out, "out", _out_bytes(dt, tokens * hidden), td))
+    td, pairs, es = _TORCH_OF.get(dt), 4 * tokens * top_k, _ES.get(dt, 1)
+    args = _addresses((y, "y", es * m * hidden, td), (row_of, "row_of", pairs, _I32),
+                      (weight, "weight", pairs, _F32), (out, "out", es * tokens * hidden, td))
     args += (tokens, hidden, top_k, m, dt)
     if validate_only:
         return lib().bsg_validate_moe_combine(*args)
@@ -696,8 +702,9 @@ def moe_combine_bwd(dout, y, row_of, padded_offsets, expert_rows, weight, dy, dw
     dweight[t, j] = <dout[t], y[row_of[t, j]]> (see include/bsg.h).  dy, or
     dweight and y, may be None."""
     dt = _code(dtype, dout)
-    td, pairs, rows = _TORCH_OF.get(dt), 4 * tokens * top_k, _out_bytes(dt, m * hidden)
-    args = _addresses((dout, "dout", _out_bytes(dt, tokens * hidden), td), (y, "y", rows, td),
+    td, pairs, es = _TORCH_OF.get(dt), 4 * tokens * top_k, _ES.get(dt, 1)
+    rows = es * m * hidden
+    args = _addresses((dout, "dout", es * tokens * hidden, td), (y, "y", rows, td),
                       (row_of, "row_of", pairs, _I32), (padded_offsets, "padded_offsets", 4 * num_experts, _I32),
                       (expert_rows, "expert_rows", 4 * num_experts, _I32), (weight, "weight", pairs, _F32),
                       (dy, "dy", rows, td), (dweight, "dweight", pairs, _F32))
@@ -712,10 +719,11 @@ def quant_fp8(x, q, scale, q_t, scale_t, m, k, l=1, tile=False, q_dtype="e4m3", 
     """x (l, m, k) -> 8-bit floats with a scale for each 128 values along k (q,
     scale) and along m (q_t, transposed, and scale_t), or with tile for each 128
     x 128 (see include/bsg.h).  Either pair may be None."""
-    xd, qd, mb, kb = _code(x_dtype, x), _fp8(q_dtype), _cdiv(m, 128), _cdiv(k, 128)
-    args = _addresses((x, "x", _out_bytes(xd, l * m * k), _TORCH_OF.get(xd)),
-                      (q, "q", l * m * k, _codes_of(q, q_dtype)), (scale, "scale", 4 * l * kb * (mb if tile else m), _F32),
-                      (q_t, "q_t", l * m * k, _codes_of(q_t, q_dtype)),
+    xd, mb, kb, n = _code(x_dtype, x), -(-m // 128), -(-k // 128), l * m * k
+    qd, qt = _fp8(q_dtype)
+    args = _addresses((x, "x", _ES.get(xd, 1) * n, _TORCH_OF.get(xd)), (q, "q", n, qt),
+                      (scale, "scale", 4 * l * kb * (mb if tile else m), _F32),
+                      (q_t, "q_t", n, qt),
                       (scale_t, "scale_t", 4 * l * mb * (kb if tile else k), _F32))
     args += (l, m, k, int(bool(tile)), xd, qd)
     if validate_only:
@@ -727,11 +735,12 @@ def gemm_fp8(a, b, a_scale, b_scale, c, m, n, k, a_dtype="e4m3", c_dtype=None, w
              validate_only=False):
     """c = a b^T from 8-bit floats with a scale for each 128 of k (a: each row,
     b: each 128 rows; see include/bsg.h)."""
-    cd, kb = _code(c_dtype, c), _cdiv(k, 128)
-    args = _addresses((a, "a", m * k, _codes_of(a, a_dtype)), (b, "b", n * k, _codes_of(b, "e4m3")),
-                      (a_scale, "a_scale", 4 * kb * m, _F32), (b_scale, "b_scale", 4 * kb * _cdiv(n, 128), _F32),
-                      (c, "c", _out_bytes(cd, m * n), _TORCH_OF.get(cd)), (workspace, "workspace", 0, None))
-    args += (_ws_bytes(workspace, "gemm_fp8", m, n, k), m, n, k, _fp8(a_dtype), cd)
+    cd, kb = _code(c_dtype, c), -(-k // 128)
+    ad, at = _fp8(a_dtype)
+    args = _addresses((a, "a", m * k, at), (b, "b", n * k, _E4M3), (a_scale, "a_scale", 4 * kb * m, _F32),
+                      (b_scale, "b_scale", 4 * kb * -(-n // 128), _F32),
+                      (c, "c", _ES.get(cd, 1) * m * n, _TORCH_OF.get(cd)), (workspace, "workspace", 0, None))
+    args += (_ws_bytes(workspace, "gemm_fp8", m, n, k), m, n, k, ad, cd)
     if validate_only:
         return lib().bsg_validate_gemm_fp8(*args)
     _check(lib().gemm_fp8(*args, _stream(stream)))
@@ -742,14 +751,14 @@ def grouped_gemm_fp8(a, b, a_scale, b_scale, padded_offsets, expert_rows, c, m, 
     """gemm_fp8 of rows sorted by expert with a weight for each expert (see
     include/bsg.h).  expert_rows may be None; max_rows: no expert has more rows
     (0: not known), for the choice of the kernel."""
-    cd, kb = _code(c_dtype, c), _cdiv(k, 128)
-    args = _addresses((a, "a", m * k, _codes_of(a, a_dtype)), (b, "b", num_experts * n * k, _codes_of(b, "e4m3")),
-                      (a_scale, "a_scale", 4 * kb * m, _F32),
-                      (b_scale, "b_scale", 4 * num_experts * kb * _cdiv(n, 128), _F32),
+    cd, kb = _code(c_dtype, c), -(-k // 128)
+    ad, at = _fp8(a_dtype)
+    args = _addresses((a, "a", m * k, at), (b, "b", num_experts * n * k, _E4M3), (a_scale, "a_scale", 4 * kb * m, _F32),
+                      (b_scale, "b_scale", 4 * num_experts * kb * -(-n // 128), _F32),
                       (padded_offsets, "padded_offsets", 4 * num_experts, _I32),
                       (expert_rows, "expert_rows", 4 * num_experts, _I32),
-                      (c, "c", _out_bytes(cd, m * n), _TORCH_OF.get(cd)))
-    args += (m, n, k, num_experts, max_rows, _fp8(a_dtype), cd)
+                      (c, "c", _ES.get(cd, 1) * m * n, _TORCH_OF.get(cd)))
+    args += (m, n, k, num_experts, max_rows, ad, cd)
     if validate_only:
         return lib().bsg_validate_grouped_gemm_fp8(*args)
     _check(lib().grouped_gemm_fp8(*args, _stream(stream)))
@@ -760,12 +769,13 @@ def grouped_gemm_fp8_wgrad(a, b, a_scale, b_scale, padded_offsets, c, m, n, k, n
     """Gradient of the experts' weights, c (num_experts, n, k), from the
     transposed codes of the output's gradient, a (n, m), and of the input, b
     (k, m) (see include/bsg.h)."""
-    cd, mb = _code(c_dtype, c), _cdiv(m, 128)
-    args = _addresses((a, "a", n * m, _codes_of(a, a_dtype)), (b, "b", k * m, _codes_of(b, "e4m3")),
-                      (a_scale, "a_scale", 4 * mb * n, _F32), (b_scale, "b_scale", 4 * mb * _cdiv(k, 128), _F32),
+    cd, mb = _code(c_dtype, c), -(-m // 128)
+    ad, at = _fp8(a_dtype)
+    args = _addresses((a, "a", n * m, at), (b, "b", k * m, _E4M3), (a_scale, "a_scale", 4 * mb * n, _F32),
+                      (b_scale, "b_scale", 4 * mb * -(-k // 128), _F32),
                       (padded_offsets, "padded_offsets", 4 * num_experts, _I32),
-                      (c, "c", _out_bytes(cd, num_experts * n * k), _TORCH_OF.get(cd)))
-    args += (m, n, k, num_experts, _fp8(a_dtype), cd)
+                      (c, "c", _ES.get(cd, 1) * num_experts * n * k, _TORCH_OF.get(cd)))
+    args += (m, n, k, num_experts, ad, cd)
     if validate_only:
         return lib().bsg_validate_grouped_gemm_fp8_wgrad(*args)
     _check(lib().grouped_gemm_fp8_wgrad(*args, _stream(stream)))

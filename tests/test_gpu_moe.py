@@ -41,7 +41,8 @@ def sort_gpu(ids, experts, m, pair_of=True, extra_ws=0):
 
 @pytest.mark.parametrize("t,k,experts", [
     (0, 2, 3), (1, 1, 1), (1, 8, 64), (16, 8, 64), (33, 3, 5), (257, 2, 1), (256, 1, 2), (100, 64, 1024), (4096, 2, 7),
-    (2049, 4, 33), (8193, 1, 256), (4001, 8, 64), (20000, 8, 128), (70001, 2, 1024)])
+    (2049, 4, 33), (4097, 1, 1),
+    (8193, 1, 256), (4001, 8, 64), (20000, 8, 128), (70001, 2, 1024), (66000, 2, 2), (300001, 1, 600)])
 def test_sort(t, k, experts):
     say("sort", t, k, experts)
     ids = routed(t, k, experts, seed=t + k)
