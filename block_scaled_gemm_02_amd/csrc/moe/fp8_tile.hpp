@@ -43,6 +43,28 @@ __device__ __forceinline__ f32x4 mfma128(const i32x8 &b, const i32x8 &a)
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, zero, 0, AE5 ? 1 : 0, 0, 0, 0, 0);
 }
 
+// lds_load16 and lds_load4 of a descriptor that a vector instruction may just have
+// written: the compiler brings scalar registers back from vector ones where it
+// ran out of them, and does not look into assembly for the 5 wait states that a
+// memory instruction then needs.  (Big, whose loads are counted out between its
+// MFMAs, has none of those; the tests look at the built code.)
+__device__ __forceinline__ void lds_load16_late(const i32x4 &rsrc, uint8_t *dst, uint32_t voff)
+{
+    const uint32_t m0 = (uint32_t)(uintptr_t)(lds_void *)dst;
+    asm volatile("s_nop 2\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(m0), "v"(voff), "s"(rsrc)
+                 : "memory", "m0");
+}
+__device__ __forceinline__ void lds_load4_late(const i32x4 &rsrc, uint8_t *dst, uint32_t voff)
+{
+    const uint32_t m0 = (uint32_t)(uintptr_t)(lds_void *)dst;
+    asm volatile("s_nop 2\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 :
+                 : "s"(m0), "v"(voff), "s"(rsrc)
+                 : "memory", "m0");
+}
+
 // What the loads of a tile take: its rows of A and of B, A's scales, and the
 // bytes of its K range.  (row 0, K block 0)
 struct Source {
@@ -134,13 +156,18 @@ struct Fp8Tile {
     __device__ __forceinline__ void load(const Source &s, int to, int kb) const
     {
         const uint32_t k = 128u * (uint32_t)kb;
+        auto load16 = [&](const i32x4 &r, uint8_t *dst, uint32_t off) {
+            if constexpr (EARLY) lds_load16(r, dst, off);
+            else lds_load16_late(r, dst, off);
+        };
         if constexpr (Q < LA + LB) {
             const uint32_t v = k + chunk < s.klimit ? voff : kOOB;
-            if constexpr (Q < LA) lds_load16(s.ra, lds + to + 1024 * (LA * w + Q), v + (8u * (LA * w + Q) * ld + k));
-            else lds_load16(s.rb, lds + to + kA + 1024 * (LB * w + Q - LA), v + (8u * (LB * w + Q - LA) * ld + k));
+            if constexpr (Q < LA) load16(s.ra, lds + to + 1024 * (LA * w + Q), v + (8u * (LA * w + Q) * ld + k));
+            else load16(s.rb, lds + to + kA + 1024 * (LB * w + Q - LA), v + (8u * (LB * w + Q - LA) * ld + k));
         } else {
             const i32x4 rs = make_rsrc_words(s.sa + kb * sa_ld, k < s.klimit ? 4u * s.rows : 0u);
-            lds_load4(rs, lds + to + kA + kB + 256 * w, voff_s);
+            if constexpr (EARLY) lds_load4(rs, lds + to + kA + kB + 256 * w, voff_s);
+            else lds_load4_late(rs, lds + to + kA + kB + 256 * w, voff_s);
         }
     }
     __device__ __forceinline__ i32x8 frag(int from, const uint32_t (&rd)[2], int off) const

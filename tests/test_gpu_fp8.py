@@ -36,6 +36,12 @@ def compare(got, a, b, sa, sb, kind, dt, name="c"):
     if kind == "whole":
         assert torch.equal(got, ref.to(dt)), (name, (got.double() - ref.to(dt).double()).abs().max())
     else:
+        if dt == F16:
+            # fp16's largest value is 65504 and its step there 32: what lies at 65520 or past it rounds to
+            # infinity, whatever the sum's error if that leaves it there
+            past = ref.abs() - err >= 65520
+            assert torch.equal(got[past].double(), ref[past].sign() * float("inf"))
+            got, ref = torch.where(past, torch.zeros_like(got), got), torch.where(past, torch.zeros_like(ref), ref)
         R.check(name, got, ref, err, dt)
         if ref.numel() >= 4096:
             # and as a whole: the roundings of C, uniform in a step, and the dropped bits, together far less
@@ -64,6 +70,101 @@ def test_gemm_fp8(m, n, k, kind):
         c = c.cpu()
         assert bool((c[0] == 5).all()) and bool((c[-1] == 5).all())
         compare(c[1:-1], a, b, sa, sb, kind, dt)
+
+
+# Large enough for each shape of tile in turn, whole and ragged, one round of
+# them and several, a last round that goes out in halves; checked on the GPU.
+LARGE = {(5000, 4096, 400): "Mid", (2049, 1032, 1040): "Mid", (4096, 4096, 1024): "Big", (4200, 4104, 1040): "Mid",
+         (2500, 4096, 1040): "Big", (5100, 4104, 2064): "Mid", (64, 512, 512): "few 64", (17, 256, 400): "few 32",
+         (16, 136, 144): "few 16", (67, 4096, 512): "Small", (40, 512, 4096): "Small / 8", (130, 2048, 7168): "Small / 5"}
+
+
+@pytest.mark.parametrize("kind", ["whole", "random"])
+@pytest.mark.parametrize("m,n,k", LARGE)
+def test_gemm_fp8_in_every_form(m, n, k, kind):
+    assert bsg.plan_string("gemm_fp8", m, n, k) == LARGE[m, n, k]
+    say("gemm_fp8", m, n, k, kind, LARGE[m, n, k])
+    g = torch.Generator().manual_seed(m + n + k)
+    fmt, dt = ("e5m2", BF) if m % 2 else ("e4m3", F16)
+    a, sa = (v.cuda() for v in operand(m, k, kind, fmt, False, g))
+    b, sb = (v.cuda() for v in operand(n, k, kind, "e4m3", True, g))
+    c = torch.full((m + 2, n), 5.0, dtype=dt, device="cuda")
+    ws = torch.empty(bsg.workspace_bytes("gemm_fp8", m, n, k), dtype=torch.uint8, device="cuda")
+    bsg.gemm_fp8(a, b, sa, sb, c[1:-1], m, n, k, a_dtype=fmt, workspace=ws)
+    assert bool((c[0] == 5).all()) and bool((c[-1] == 5).all())
+    compare(c[1:-1], a, b, sa, sb, kind, dt)
+
+
+@pytest.mark.parametrize("kind", ["whole", "random"])
+def test_grouped_gemm_fp8_in_large_tiles(kind):
+    """256 x 256 tiles, in two rounds and a part, of uneven experts."""
+    counts, m, n, k = [3000, 0, 1, 257, 5000, 128, 129, 2600, 4000], 17408, 2048, 2064
+    g = torch.Generator().manual_seed(5)
+    ends, rows = offsets_of(counts, m)
+    a, sa = (v.cuda() for v in operand(m, k, kind, "e4m3", False, g))
+    bs = [[v.cuda() for v in operand(n, k, kind, "e4m3", True, g)] for _ in counts]
+    b, sb = torch.stack([x[0] for x in bs]), torch.stack([x[1] for x in bs])
+    for use_rows in (True, False):
+        say("grouped_gemm_fp8 large", kind, use_rows)
+        c = torch.full((m, n), 5.0, dtype=BF, device="cuda")
+        bsg.grouped_gemm_fp8(a, b, sa, sb, ends.cuda(), rows.cuda() if use_rows else None, c, m, n, k, len(counts),
+                             max_rows=max(counts))
+        at = 0
+        for e, (x, s) in enumerate(bs):
+            end = int(ends[e])
+            last = at + counts[e] if use_rows else end
+            if last > at:
+                compare(c[at:last], a[at:last], x, sa[:, at:last], s, kind, BF, f"expert {e}")
+            assert bool((c[last:end] == 5).all())
+            at = end
+        assert bool((c[at:] == 5).all())
+
+
+@pytest.mark.parametrize("kind", ["whole", "random"])
+def test_grouped_gemm_fp8_wgrad_in_large_tiles(kind):
+    counts, m, n, k = [3000, 0, 700, 256, 1500, 40], 6400, 2056, 2064
+    g = torch.Generator().manual_seed(6)
+    ends, rows = offsets_of(counts, m)
+    a, sa = operand(n, m, kind, "e5m2", False, g)
+    b, sb = operand(k, m, kind, "e4m3", True, g)
+    a.view(torch.uint8)[:, R.held_rows(ends, rows, m) == 1] = 0
+    a, sa, b, sb = a.cuda(), sa.cuda(), b.cuda(), sb.cuda()
+    say("wgrad large", kind)
+    c = torch.full((len(counts), n, k), 5.0, dtype=BF, device="cuda")
+    bsg.grouped_gemm_fp8_wgrad(a, b, sa, sb, ends.cuda(), c, m, n, k, len(counts), a_dtype="e5m2")
+    at = 0
+    for e, end in enumerate(ends.tolist()):
+        if end == at:
+            assert bool((c[e] == 0).all())
+        else:
+            compare(c[e], a[:, at:end], b[:, at:end], sa[at // 128:end // 128], sb[:, at // 128:end // 128], kind, BF)
+        at = end
+
+
+def test_gemm_fp8_long_k():
+    """More than 64 blocks, whose scales of B a wave holds, twice over."""
+    for m, n, k in ((3, 128, 20000), (300, 264, 20000)):
+        say("gemm_fp8", m, n, k)
+        g = torch.Generator().manual_seed(k)
+        a, sa = operand(m, k, "whole", "e4m3", False, g)
+        b, sb = operand(n, k, "whole", "e4m3", True, g)
+        c = torch.empty(m, n, dtype=BF, device="cuda")
+        ws = torch.empty(bsg.workspace_bytes("gemm_fp8", m, n, k), dtype=torch.uint8, device="cuda")
+        bsg.gemm_fp8(a.cuda(), b.cuda(), sa.cuda(), sb.cuda(), c, m, n, k, workspace=ws)
+        compare(c.cpu(), a, b, sa, sb, "whole", BF)
+
+
+def test_grouped_long_k_large_tiles():
+    m, n, k = 8192, 4096, 9232
+    g = torch.Generator().manual_seed(8)
+    ends, rows = offsets_of([8000], m)
+    a, sa = (v.cuda() for v in operand(m, k, "whole", "e4m3", False, g))
+    b, sb = (v.cuda() for v in operand(n, k, "whole", "e4m3", True, g))
+    c = torch.full((m, n), 5.0, dtype=F16, device="cuda")
+    say("grouped long k")
+    bsg.grouped_gemm_fp8(a, b[None], sa, sb[None], ends.cuda(), rows.cuda(), c, m, n, k, 1)
+    compare(c[:8000], a[:8000], b, sa[:, :8000], sb, "whole", F16)
+    assert bool((c[8000:] == 5).all())
 
 
 def test_gemm_fp8_of_nothing():
