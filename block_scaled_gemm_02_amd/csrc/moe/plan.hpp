@@ -17,11 +17,12 @@ struct Plan {
 
 // Estimates in microseconds, from times measured on the card (256 compute
 // units):
-//   * a block of 128 of K takes a Big tile 1.15 us while at most half the
+//   * a block of 128 of K takes a Big tile 1.15 us where little more than half the
 //     compute units are at work (2048 cycles of MFMA) and 1.5 us with all of them
-//     (the clock falls under the power limit); Mid tiles, two a unit, 0.70 and 1.05
-//     us; a Small one 0.35 and 0.41 us, and in parts, two a unit, 0.60 us: its
-//     loads bound it, not its 256 cycles of MFMA;
+//     (the clock falls under the power limit); at most 128 tiles go out in halves
+//     of 0.85 us; Mid tiles, two a unit, 0.70 and 1.05 us; a Small one 0.35 and 0.41
+//     us, and in parts, two a unit, 0.60 us: its loads bound it, not its 256 cycles
+//     of MFMA;
 //   * launch, first loads and the way out take 7.0, 3.0 and 3.8 us, each further
 //     round of tiles 5.2, 2.1 and 1.3 us more;
 //   * the operands come from memory at 4.9 TB/s (and 3.5 us of launch);
@@ -29,16 +30,20 @@ struct Plan {
 //     memory and back at 2.2 TB/s of them.
 // Measured (us, Big / Mid / Small / Small in parts, operands in the memory-side
 // cache): 64 x 4096, K 7168 - / 33.3 / 23.0 / 13.2 (4); 256 x 4096, K 7168 - /
-// 42.4 / 23.5 / 19.9 (2); 1024 x 2048, K 7168 75.5 / 42.4 / 25.4 / 34.5 (2); 512
-// x 4096, K 4096 44.5 / 24.7 / 16.9 / 24.3 (2); 2048 x 4096, K 2048 25.4 / 20.6 /
-// 31.9 / -; 2048 x 2048, K 8192 80.6 / 47.0 / 54.1 / -; 3000 x 4096, K 7168 78.6
-// / 95.1 / 137 / -; 8192^3 410 / 533 / 694 / -.
+// 42.4 / 23.5 / 19.9 (2); 1024 x 2048, K 7168 - / 42.4 / 25.4 / 34.5 (2); 512 x
+// 4096, K 4096 - / 24.7 / 16.9 / 24.3 (2); 2048 x 4096, K 2048 19.7 / 20.7 / 31.9 /
+// -; 4096 x 2048, K 4096 34.1 / 35.5 / 56.6 / -; 2500 x 4096, K 1040 18.6 / 20.1 / -
+// / -; 4200 x 4104, K 2064 57.3 / 59.3 / - / -; 5000 x 4096, K 4096 80.8 (94.2 with
+// a whole last round) / 89.3 / - / -; 6000 x 704, K 512 10.7 / 7.8 / 11.5 / -;
+// 8192^3 410 / 533 / 694 / -.
 struct ShapeCost {
     int tm, tn, per_cu;
     double fixed, round, block, block_all;
 };
 static constexpr ShapeCost kCost[3] = {
     {256, 256, 1, 7.0, 5.2, 1.15, 1.5}, {128, 128, 2, 3.0, 2.1, 0.70, 1.05}, {64, 128, 1, 3.8, 1.3, 0.35, 0.41}};
+
+static constexpr double kHalf = 0.85;       // a half of a Big tile
 
 // groups: products of these sizes (experts), each with its own sum over k.
 inline Plan plan_with(int shape, int splits, int64_t rows, int64_t cols, int64_t k, int64_t groups)
@@ -49,7 +54,9 @@ inline Plan plan_with(int shape, int splits, int64_t rows, int64_t cols, int64_t
     const int64_t tiles = (rows + c.tm - 1) / c.tm * ((cols + c.tn - 1) / c.tn) * groups * splits, wave = 256 * per_cu;
     const int64_t full = tiles / wave, rest = tiles % wave;
     const double blocks = (double)((ffn::pairs_in(k) + splits - 1) / splits);
-    const double part = rest > wave / 2 ? c.block + (all - c.block) * (double)(2 * rest - wave) / (double)wave : c.block;
+    const double part = rest > wave / 2    ? c.block + (all - c.block) * (double)(2 * rest - wave) / (double)wave
+                        : shape == BIG && groups == 1 ? kHalf
+                                                      : c.block;
     double t = c.fixed + (double)(full + (rest > 0) - 1) * c.round + blocks * ((double)full * all + (rest ? part : 0));
     t = std::max(t, 3.5 + (double)groups * (double)(rows + cols) * (double)k / 4.9e6);
     if (splits > 1) t += 1.5 + (double)rows * (double)cols * splits * 4 / 2.2e6;

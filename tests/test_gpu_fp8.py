@@ -74,9 +74,10 @@ def test_gemm_fp8(m, n, k, kind):
 
 # Large enough for each shape of tile in turn, whole and ragged, one round of
 # them and several, a last round that goes out in halves; checked on the GPU.
-LARGE = {(5000, 4096, 400): "Mid", (2049, 1032, 1040): "Mid", (4096, 4096, 1024): "Big", (4200, 4104, 1040): "Mid",
-         (2500, 4096, 1040): "Big", (5100, 4104, 2064): "Mid", (64, 512, 512): "few 64", (17, 256, 400): "few 32",
-         (16, 136, 144): "few 16", (67, 4096, 512): "Small", (40, 512, 4096): "Small / 8", (130, 2048, 7168): "Small / 5"}
+LARGE = {(5000, 4096, 400): "Mid", (2049, 1032, 1040): "Mid", (4200, 4104, 1040): "Mid", (4096, 4096, 1024): "Big",
+         (2500, 4096, 1040): "Big", (4200, 4104, 2064): "Big", (5100, 4104, 2064): "Big", (64, 512, 512): "few 64",
+         (17, 256, 400): "few 32", (16, 136, 144): "few 16", (67, 4096, 512): "Small", (40, 512, 4096): "Small / 8",
+         (130, 2048, 7168): "Small / 5"}
 
 
 @pytest.mark.parametrize("kind", ["whole", "random"])

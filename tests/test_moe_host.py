@@ -227,3 +227,24 @@ def test_reference_gradients_match_differences():
         lo = fun(*args)
         v[at] = old
         assert abs((hi - lo) / 2 - float(grad[at])) < 1e-9
+
+
+@pytest.mark.parametrize("m", [1, 2, 16, 17, 40, 64, 65, 300, 1000, 4096, 8192])
+def test_gemm_fp8_plan(m):
+    """Every size has a form; parts of K have room for their sums and none is too short."""
+    seen = set()
+    for n in (8, 128, 1000, 4096, 8192):
+        for k in (0, 16, 512, 2048, 7168, 16384):
+            text = bsg.plan_string("gemm_fp8", m, n, k)
+            form, _, parts = text.partition(" / ")
+            assert form in ("few 16", "few 32", "few 64", "Small", "Mid", "Big")
+            if form.startswith("few"):
+                assert m <= int(form[4:]) <= max(16, 2 * m)
+            need = bsg.workspace_bytes("gemm_fp8", m, n, k)
+            assert need == (4 * m * n * int(parts) if parts else 0)
+            assert not parts or (form == "Small" and k >= 128 * 4 * int(parts) - 127)
+            seen.add(form)
+    assert ("Big" in seen) == (m >= 1000) or m == 1000
+    assert bsg.plan_string("gemm_fp8", 0, 64, 64) == "none"
+    with pytest.raises(ValueError):
+        bsg.plan_string("moe_sort", 1, 1, 1)
