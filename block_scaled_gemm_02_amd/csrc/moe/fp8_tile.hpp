@@ -347,7 +347,7 @@ struct Fp8Tile {
         });
     }
 
-    // run() of a wave whose rows lie behind the tile's last one: its share of the
+    // run() of a wave that has no row or no column of the tile: its share of the
     // loads, and the barriers.  The waves that have rows then have the matrix
     // cores to themselves.
     __device__ __forceinline__ void run_idle(Source src, const Source &next, int count)

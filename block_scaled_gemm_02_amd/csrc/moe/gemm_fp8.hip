@@ -220,7 +220,8 @@ __global__ __launch_bounds__(T::kThreads, T::kWaves) void k_fp8(Fp8Args p, unsig
         more = walk.take(then);
         if (!more) then.src.klimit = 0;         // nothing after the last tile
         const int blocks = (int)((cur.src.klimit + 127) / 128), count = T::count_of(blocks);
-        if (cur.to.rows <= 16 * T::WM * tile.wm) {
+        // (a wave past the last column would also read scales past B's last ones)
+        if (cur.to.rows <= 16 * T::WM * tile.wm || cur.to.cols <= 16 * T::WN * tile.wn) {
             tile.run_idle(cur.src, then.src, count);
             if (!more) s_wait_vm<0>();
         } else {
