@@ -111,20 +111,34 @@ __global__ __launch_bounds__(256) void k_combine(CombineArgs p, int lg, int64_t 
     }
     if (col >= pieces || !p.out) return;
     float acc[N] = {};
-    for (int j = 0; j < p.top_k; ++j) {
-        const int r = row_at(p.row_of, t * p.top_k + j, p.m);
-        if (r < 0) continue;
-        Piece<DT, N> y;
-        y.load((const u32x4 *)p.y + r * pieces + col);
-        const float w = WEIGHT ? p.weight[t * p.top_k + j] : 1.0f;
+    // four choices at a time, their rows under way together
+    for (int j0 = 0; j0 < p.top_k; j0 += 4) {
+        int r[4];
+        float w[4];
+        Piece<DT, N> y[4];
 #pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] = WEIGHT ? fmaf(w, y.at(i), acc[i]) : acc[i] + y.at(i);
+        for (int j = 0; j < 4; ++j) {
+            const int64_t pair = t * p.top_k + j0 + j;
+            r[j] = j0 + j < p.top_k ? row_at(p.row_of, pair, p.m) : -1;
+            w[j] = WEIGHT && j0 + j < p.top_k ? p.weight[pair] : 1.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (r[j] >= 0) y[j].load((const u32x4 *)p.y + r[j] * pieces + col);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (r[j] < 0) continue;
+#pragma unroll
+            for (int i = 0; i < N; ++i) acc[i] = WEIGHT ? fmaf(w[j], y[j].at(i), acc[i]) : acc[i] + y[j].at(i);
+        }
     }
     ((u32x4 *)p.out)[t * pieces + col] = pack16<DT>(acc);
 }
 
-// dy[row] = weight dout[t] and dweight = <dout[t], y[row]>.
-template <int DT>
+// dy[row] = weight dout[t] and dweight = <dout[t], y[row]>, J choices at a
+// time, so that a piece of dout is read once for them and their rows are under
+// way together.
+template <int DT, int J>
 __global__ __launch_bounds__(256) void k_combine_bwd(CombineBwdArgs p, int lg, unsigned rows_grid, int64_t pieces)
 {
     constexpr int N = 16 / es_dt(DT);
@@ -136,39 +150,66 @@ __global__ __launch_bounds__(256) void k_combine_bwd(CombineBwdArgs p, int lg, u
             for (int64_t c = c0; c < pieces; c += tpr) dy[r * pieces + c] = u32x4{0, 0, 0, 0};
         return;
     }
-    __shared__ float part[4];
+    __shared__ float part[J][4];
     const int64_t t = (int64_t)blockIdx.x * per + sub;
     const bool in = t < p.tokens;
-    for (int j = 0; j < p.top_k; ++j) {
-        const int64_t pair = t * p.top_k + j;
-        const int r = in ? row_at(p.row_of, pair, p.m) : -1;
-        const float w = r >= 0 ? p.weight[pair] : 0.0f;
-        float dot = 0.0f;
-        if (r >= 0)
+    for (int j0 = 0; j0 < p.top_k; j0 += J) {
+        int r[J];
+        float w[J], dot[J];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int64_t pair = t * p.top_k + j0 + j;
+            r[j] = in && j0 + j < p.top_k ? row_at(p.row_of, pair, p.m) : -1;
+            w[j] = r[j] >= 0 && p.weight ? p.weight[pair] : 1.0f;
+            dot[j] = 0.0f;
+        }
+        if (in)
             for (int64_t c = c0; c < pieces; c += tpr) {
-                Piece<DT, N> d, y;
+                Piece<DT, N> d, y[J];
                 d.load((const u32x4 *)p.dout + t * pieces + c);
                 if (p.dweight) {
-                    y.load((const u32x4 *)p.y + r * pieces + c);
 #pragma unroll
-                    for (int i = 0; i < N; ++i) dot = fmaf(d.at(i), y.at(i), dot);
+                    for (int j = 0; j < J; ++j) {
+                        y[j].zero();
+                        if (r[j] >= 0) y[j].load((const u32x4 *)p.y + r[j] * pieces + c);
+                    }
+                    // (what is not a row of a pair counts as nothing, also where dout is not finite)
+#pragma unroll
+                    for (int j = 0; j < J; ++j)
+#pragma unroll
+                        for (int i = 0; i < N; ++i) dot[j] = r[j] >= 0 ? fmaf(d.at(i), y[j].at(i), dot[j]) : 0.0f;
                 }
                 if (dy) {
-                    float o[N];
 #pragma unroll
-                    for (int i = 0; i < N; ++i) o[i] = w * d.at(i);
-                    dy[r * pieces + c] = pack16<DT>(o);
+                    for (int j = 0; j < J; ++j) {
+                        if (r[j] < 0) continue;
+                        float o[N];
+#pragma unroll
+                        for (int i = 0; i < N; ++i) o[i] = w[j] * d.at(i);
+                        dy[r[j] * pieces + c] = pack16<DT>(o);
+                    }
                 }
             }
         if (!p.dweight) continue;
-        for (int d = min(tpr, 64) / 2; d; d >>= 1) dot += __shfl_xor(dot, d);
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            for (int d = min(tpr, 64) / 2; d; d >>= 1) dot[j] += __shfl_xor(dot[j], d);
         if (tpr > 64) {
             __syncthreads();
-            if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = dot;
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                if ((threadIdx.x & 63) == 0) part[j][threadIdx.x >> 6] = dot[j];
             __syncthreads();
-            dot = tpr == 128 ? part[2 * sub] + part[2 * sub + 1] : (part[0] + part[1]) + (part[2] + part[3]);
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const float *const q = part[j];
+                dot[j] = tpr == 128 ? q[2 * sub] + q[2 * sub + 1] : (q[0] + q[1]) + (q[2] + q[3]);
+            }
         }
-        if (in && c0 == 0) p.dweight[pair] = dot;
+        if (in && c0 == 0)
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                if (j0 + j < p.top_k) p.dweight[t * p.top_k + j0 + j] = dot[j];
     }
 }
 
@@ -212,7 +253,10 @@ hipError_t launch_moe_combine_bwd(const CombineBwdArgs &a, hipStream_t s)
     const Lay l = lay_of(a.tokens, pieces, 4);
     if (l.rows + pads == 0) return hipSuccess;
     with_float(a.dtype, [&](auto dt) {
-        k_combine_bwd<decltype(dt)::value><<<l.rows + pads, 256, 0, s>>>(a, l.lg, l.rows, pieces);
+        // (as many at a time as a token has, up to 8)
+        if (a.top_k <= 2) k_combine_bwd<decltype(dt)::value, 2><<<l.rows + pads, 256, 0, s>>>(a, l.lg, l.rows, pieces);
+        else if (a.top_k <= 4) k_combine_bwd<decltype(dt)::value, 4><<<l.rows + pads, 256, 0, s>>>(a, l.lg, l.rows, pieces);
+        else k_combine_bwd<decltype(dt)::value, 8><<<l.rows + pads, 256, 0, s>>>(a, l.lg, l.rows, pieces);
     });
     return hipGetLastError();
 }
