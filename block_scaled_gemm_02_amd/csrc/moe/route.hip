@@ -3,6 +3,13 @@
 // token's choice j, or -1; every row belongs to one pair at most, so all sums
 // run over a token's own choices, in their order, and nothing is added
 // atomically.
+//
+// A token's workgroups read it once and write each of its rows (or read each and
+// write it once): memory bounds them.  4001 tokens of 7168 bf16 to E4M3 rows, 8
+// each (270 MB) 57 us with the sort, 46 us without it; 8192 of 4096 bf16 to 8 rows
+// each, padding zeroed (640 MB) 113 us; their gradients back (604 MB) 116 us, 5.2
+// TB/s; moe_combine's gradients (1.21 GB) 232 us, 5.2 TB/s (a large copy reaches
+// 4.5-4.7).  Few tokens are bound by the launch: 33 of 7168 fp16 4.7 us.
 #include "rows.hpp"
 
 namespace bsg {
@@ -49,7 +56,7 @@ __global__ __launch_bounds__(256) void k_gather(GatherArgs p, int lg, unsigned r
     for (int j = 0; j < p.top_k; ++j) {
         const int r = row_at(p.row_of, t * p.top_k + j, p.m);
         if (r < 0) continue;
-        y[r * pieces + col] = x;
+        store_past(y + r * pieces + col, x);
         if (col == 0 && p.prob) p.prob[r] = p.weight[t * p.top_k + j];
     }
 }
@@ -88,7 +95,7 @@ __global__ __launch_bounds__(256) void k_gather_fp8(GatherArgs p, int lg, unsign
     for (int j = 0; j < p.top_k; ++j) {
         const int r = row_at(p.row_of, t * p.top_k + j, p.m);
         if (r < 0) continue;
-        y[r * pieces + col] = q;
+        store_past(y + r * pieces + col, q);
         if (first) sc[r] = s.scale;
         if (col == 0 && p.prob) p.prob[r] = p.weight[t * p.top_k + j];
     }
@@ -186,7 +193,7 @@ __global__ __launch_bounds__(256) void k_combine_bwd(CombineBwdArgs p, int lg, u
                         float o[N];
 #pragma unroll
                         for (int i = 0; i < N; ++i) o[i] = w[j] * d.at(i);
-                        dy[r[j] * pieces + c] = pack16<DT>(o);
+                        store_past(dy + r[j] * pieces + c, pack16<DT>(o));
                     }
                 }
             }
