@@ -10,21 +10,39 @@
 // result cannot stay in the matrix core, because each row's factor changes from
 // block to block, so it comes out and is added with a multiply-add for each
 // value.  Those take half the vector unit's time at the matrix cores' full rate
-// and run beside the MFMAs, but they need the sums in plain registers, which
-// bounds a wave to 128 x 64: twelve instructions' registers move between
-// AGPRs and VGPRs otherwise.  B is the MFMA's first operand, so that a lane
-// holds four columns of one row and needs one factor for 16 rows.
+// and run beside the MFMAs, but they need the sums in vector registers: from
+// AGPRs each value would take two moves more, past the MFMA's own time.  That
+// bounds a wave to 128 x 64.  B is the MFMA's first operand, so that a lane holds
+// four columns of one row and needs one factor for them.
 //
 // The LDS holds a ring of slots, a K block of A, of B and of A's scales each,
 // filled by direct-to-LDS loads; reads past a row, a tensor or the K range
 // return zeros (buffer range check).  128 bytes of K are one line of a row; its
 // 16-byte chunk c lies at c ^ s(r), so that a fragment read meets every bank
-// once (ffn/tile.hpp).  A lane's scales, rows r, r + 16, ... of the wave's, lie
-// beside each other.
-// One barrier a block, two rows of MFMAs before its end: by then every wave has
-// the block's last fragments in registers, and the next block has landed.
-// Behind it the slot is filled again, and the next block's first fragments are
-// read between the MFMAs of the last ones.
+// once (ffn/tile.hpp), and a lane's scales, rows r, r + 16, ... of the wave's, lie
+// four together on banks that 16 lanes share out (two rows of lanes on the same
+// banks took 27 cycles a block and wave).
+//
+// The largest tile (256 x 256, EARLY) has two slots.  A wave holds one block's
+// columns and four of its eight rows of fragments (240 of 256 registers), and
+// a block has two barriers.  At its second row of MFMAs every wave has the
+// columns in registers, and B's part of the slot is filled again; three rows before
+// its end every wave has the last row, the next block has landed, and A's part
+// follows, while the next block's fragments are read between the last MFMAs.  So
+// B's loads have 1.75 blocks to land and A's one.  With B filled again beside A,
+// weights from HBM came too late: 32 experts of 4096 x 7168, 32768 rows 873 us for
+// 813, 64 experts of that with 4 rows each 372 us for 318 (5.9 TB/s).  Half of A
+// early too (the barrier then has to wait for its reads), loads all in one row of
+// MFMAs, or lines prefetched into the L2 cost 2 to 7%.  The last three results of
+// a block are added in the next one, so that no wave waits for them.
+// The smallest (64 x 128, WHOLE) holds two blocks' fragments and has one barrier
+// a block, at its beginning (25.6 us for 23.5 at 56 blocks).
+//
+// A workgroup's tiles follow each other in the ring.  What bounds the largest
+// one: with all compute units at work the power limit; 8192^3 takes 407-425 us by
+// card, 2590-2700 TFLOP/s, the matrix cores 67% busy at the clock that is left (on
+// zeros 320 us; without the multiply-adds 9% less).  Each tile's way out costs 5
+// us, 128 KB of C a compute unit.
 #pragma once
 #include "../ffn/tile.hpp"
 #include "rows.hpp"
@@ -102,9 +120,9 @@ struct Fp8Tile {
     // one block's columns and kRing of its rows, where two do not fit.
     static constexpr bool WHOLE = WM < 4;
     static constexpr int kRing = WHOLE ? WM : 4, kAhead = WHOLE ? WM : 3;
-    // B's share of a slot is free, and filled again, when its columns are in
-    // registers, a block's length before A's
+    // B's share of a slot is free, and filled again, when its columns are in registers
     static constexpr bool EARLY = WM >= 8;
+    static constexpr int kStores = WM * WN / 2;                                 // of a wave, at the end of a tile
     static constexpr int kMin = WHOLE ? (S + 1) / 2 * 2 : S;                    // least blocks of a tile
     static constexpr int N = WM * WN;
     static_assert(128 % (16 * WN) == 0, "a wave's columns lie in one 128");
@@ -198,7 +216,7 @@ struct Fp8Tile {
         static_for<S>([&](auto n) {
             static_for<L>([&](auto q) { load<decltype(q)::value>(s, decltype(n)::value * kSlot, decltype(n)::value); });
         });
-        s_wait_vm<(S - 1) * L>();
+        s_wait_vm<EARLY ? 0 : (S - 1) * L>();
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
     }
@@ -212,13 +230,11 @@ struct Fp8Tile {
 
     // acc = sum over the `count` blocks of a tile, the first of which has landed,
     // as has that of the next tile, whose loads come from `next`, in the end.  sb:
-    // B's scales of the wave's columns, nsb of them.
+    // B's scales of the wave's columns, nsb of them; sbv: the first 64, one a lane.
     template <bool AE5>
     __device__ __forceinline__ void run(f32x4 (&acc)[WM][WN], Source src, const Source &next, int count,
-                                        const float *sb, int nsb)
+                                        const float *sb, int nsb, float sbv)
     {
-        // B's scales of 64 blocks, one a lane
-        float sbv = lane < nsb ? sb[lane] : 0.0f;
         auto scale_b = [&](int i) { return __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(sbv), i & 63)); };
 #pragma unroll
         for (int i = 0; i < WM; ++i)
@@ -247,10 +263,11 @@ struct Fp8Tile {
             if constexpr (m >= 3) add<m - 3>(acc, f[(m - 3) / WN], t);
             else add<N - 3 + m>(acc, old[WM - 1 - (N - 3 + m) / WN], t);
         };
-        auto barrier = [&] {
+        auto barrier = [&](auto first) {
             // this block's fragments are in registers, the next block has landed
             s_wait_lgkm0();
-            s_wait_vm<(S - 2) * L + (EARLY ? LB : 0)>();
+            if constexpr (decltype(first)::value) s_wait_vm<LB + kStores>();
+            else s_wait_vm<(S - 2) * L + (EARLY ? LB : 0)>();
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_sched_barrier(0);
         };
@@ -272,7 +289,7 @@ struct Fp8Tile {
                 const int fill = n + S < count ? n + S : n + S - count;
                 if (fill == 0) src = next;
                 set_factors(cur, n);
-                barrier();
+                barrier(std::false_type{});
                 constexpr int R = 1 + WN + WM, span = N * 3 / 4;
                 static_for<N>([&](auto mm) {
                     constexpr int m = decltype(mm)::value, i = m / WN, j = m % WN;
@@ -297,7 +314,11 @@ struct Fp8Tile {
             }
         } else {
             set_factors(fr, 0);
-            for (int n = 0; n < count; ++n) {
+            // first: a tile's first block.  Its successor's loads went out before the
+            // wave's stores of the tile before, which memory instructions, returning in
+            // order, need not be waited for; or it has landed (start, run_idle).
+            // (weight gradient of 32 x 512 rows, 4096 x 2048: 164 us for 167.5)
+            auto step = [&](auto first, int n) {
                 const int to = at == (S - 1) * kSlot ? 0 : at + kSlot;
                 refill_scales(n + 1);
                 const int fill = n + S < count ? n + S : n + S - count;
@@ -309,7 +330,7 @@ struct Fp8Tile {
                         __builtin_amdgcn_s_barrier();
                         __builtin_amdgcn_sched_barrier(0);
                     }
-                    if constexpr (i == WM - kAhead && j == 0) barrier();
+                    if constexpr (i == WM - kAhead && j == 0) barrier(first);
                     mfma(mm, fr.b[j], fr.a[i % kRing]);
                     // the fragment kAhead rows on, this block's or the next one's
                     if constexpr (j == 0) {
@@ -339,7 +360,9 @@ struct Fp8Tile {
                 keep_factors();
                 set_factors(fr, n + 1);
                 at = to;
-            }
+            };
+            step(std::bool_constant<EARLY>{}, 0);
+            for (int n = 1; n < count; ++n) step(std::false_type{}, n);
         }
         static_for<3>([&](auto mm) {
             constexpr int m = N - 3 + decltype(mm)::value;
@@ -366,6 +389,7 @@ struct Fp8Tile {
             load<LA + LB>(src, at, fill);
             at = at == (S - 1) * kSlot ? 0 : at + kSlot;
         }
+        if constexpr (EARLY) s_wait_vm<0>();
     }
     // acc to C, 16 rows at a time through LDS of its own, so that whole lines are
     // stored.
@@ -395,6 +419,7 @@ struct Fp8Tile {
             });
 #pragma unroll
             for (int k = 0; k < 16 / RPI; ++k) {
+                static_assert(WM * (16 / RPI) == kStores, "run() counts them");
                 const i32x4 v = *(const i32x4 *)(reg + (lr + k * RPI) * kRow + cb);
                 __builtin_amdgcn_raw_buffer_store_b128(v, rs, voff + (uint32_t)(16 * i + k * RPI) * row_bytes, 0, kNT);
             }
