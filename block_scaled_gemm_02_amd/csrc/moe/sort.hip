@@ -15,7 +15,7 @@
 // launch that leaves each chunk's counts in the workspace, 512 pairs a chunk up to
 // 131072 pairs, so that a wave has its ids in one load each, and a chunk's
 // workgroup sums the counts of the others in parallel slices.
-// Bound by latency: 128 pairs 4.6 us, launch included; 32008 pairs over 64
+// Bound by latency: 128 pairs 5.1 us, launch included; 32008 pairs over 64
 // experts 13.5 us with 2048 pairs a chunk and one thread an expert, 11.4 us so.
 #include "rows.hpp"
 
