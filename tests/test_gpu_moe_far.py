@@ -151,3 +151,36 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for side in sides:
         assert torch.equal(side[5], side[4])
+
+
+def test_wgrad_of_the_most_rows():
+    """Operands with 2^22 bytes between their rows; the last expert's range is at their end."""
+    m, n, k, last = 1 << 22, 264, 520, 512
+    print("wgrad of 2^22 rows", flush=True)
+    g = torch.Generator().manual_seed(7)
+    a, b = (torch.zeros(r, m, dtype=torch.float8_e4m3fn, device=DEV) for r in (n, k))
+    sa, sb = torch.zeros(m // 128, n, device=DEV), torch.zeros(-(-k // 128), m // 128, device=DEV)
+    x, sx = whole(n, last, False, g)
+    w, sw = whole(k, last, True, g)
+    a[:, m - last:], sa[-last // 128:], b[:, m - last:], sb[:, -last // 128:] = x.cuda(), sx.cuda(), w.cuda(), sw.cuda()
+    ends = torch.tensor([m - last, m - last, m], dtype=torch.int32, device=DEV)
+    c = torch.full((4, n, k), 5.0, dtype=BF, device=DEV)
+    bsg.grouped_gemm_fp8_wgrad(a, b, sa, sb, ends, c[:3], m, n, k, 3)
+    want = (R.values(x, sx, False).cuda() @ R.values(w, sw, True).cuda().t()).to(BF)
+    assert bool((c[:2] == 0).all()) and torch.equal(c[2], want) and bool((c[3] == 5).all())
+
+
+def test_product_of_the_most_rows():
+    """2^22 rows: the last begin past 4 GiB of A and of C."""
+    m, n, k, last = 1 << 22, 1032, 1040, 300
+    print("product of 2^22 rows", bsg.plan_string("gemm_fp8", m, n, k), flush=True)
+    g = torch.Generator().manual_seed(8)
+    a, sa = torch.zeros(m, k, dtype=torch.float8_e4m3fn, device=DEV), torch.zeros(-(-k // 128), m, device=DEV)
+    x, sx = whole(last, k, False, g)
+    b, sb = whole(n, k, True, g)
+    a[m - last:], sa[:, m - last:] = x.cuda(), sx.cuda()
+    c = torch.full((m, n), 5.0, dtype=BF, device=DEV)
+    ws = torch.empty(bsg.workspace_bytes("gemm_fp8", m, n, k), dtype=torch.uint8, device=DEV)
+    bsg.gemm_fp8(a, b.cuda(), sa, sb.cuda(), c, m, n, k, workspace=ws)
+    want = (R.values(x, sx, False).cuda() @ R.values(b, sb, True).cuda().t()).to(BF)
+    assert torch.equal(c[m - last:], want) and not bool(c[:m - last].any())

@@ -137,6 +137,7 @@ def test_fp8_product_validation(f):
 def test_fp8_product_sizes():
     assert gemm(k=24) == ALIGN and gemm(n=12) == ALIGN and gemm(n=8, k=16) == OK and gemm(k=0, a=0, b=0, a_scale=0) == OK
     assert gemm(m=1 << 22, n=1 << 20) == UNSUP
+    assert gemm(m=(1 << 22) + 1, n=8) == UNSUP and gemm(k=(1 << 20) + 16) == UNSUP and grouped(m=(1 << 22) + 256) == UNSUP
     parts = dict(m=130, n=2048, k=7168)                   # K in parts: a workspace is needed
     assert gemm(**parts) == OK and gemm(**parts, workspace=None) == NULLPTR and gemm(**parts, workspace=P + 4) == ALIGN
     assert grouped(k=24) == ALIGN and grouped(n=12) == ALIGN and grouped(m=1000) == SHAPE and grouped(num_experts=0) == SHAPE
