@@ -6,6 +6,11 @@ import subprocess
 import sys
 from concurrent.futures import ThreadPoolExecutor
 
+try:
+    from . import wait_states
+except ImportError:         # run as a script
+    import wait_states
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libbsg.so")
@@ -48,6 +53,8 @@ def build(verbose: bool = True) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}{r.stderr}")
+    # hand-written loads wait for their descriptors, or there is no library
+    wait_states.check(tmp)
     os.replace(tmp, OUT)
     if verbose:
         print(f"built {OUT}")

@@ -64,8 +64,10 @@ __device__ __forceinline__ f32x4 mfma128(const i32x8 &b, const i32x8 &a)
 // lds_load16 and lds_load4 of a descriptor that a vector instruction may just have
 // written: the compiler brings scalar registers back from vector ones where it
 // ran out of them, and does not look into assembly for the 5 wait states that a
-// memory instruction then needs.  (Big, whose loads are counted out between its
-// MFMAs, has none of those; the tests look at the built code.)
+// memory instruction then needs.  The largest tile takes the loads without them:
+// between its MFMAs they cost 1.5 to 2.5% (8192^3 427 -> 437 us, 8192 tokens
+// through 32 experts 886 -> 906), and the compiler restores its descriptors long
+// before.  That is no promise, so the build checks every load (wait_states.py).
 __device__ __forceinline__ void lds_load16_late(const i32x4 &rsrc, uint8_t *dst, uint32_t voff)
 {
     const uint32_t m0 = (uint32_t)(uintptr_t)(lds_void *)dst;
