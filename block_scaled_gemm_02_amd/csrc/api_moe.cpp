@@ -118,8 +118,10 @@ int bsg_validate_moe_gather(const void *x, const int32_t *row_of, const int32_t 
     if (y_dtype != x_dtype && y_dtype != BSG_E4M3)
         return fail(BSG_ERR_DTYPE, "y_dtype %d is neither x's nor E4M3", y_dtype);
     if (int r = check_hidden(hidden, y_dtype == BSG_E4M3 ? 16 : 16 / elem_bytes(x_dtype))) return r;
-    if (!weight != !prob) return fail(BSG_ERR_NULLPTR, "weight and prob are given together or not at all");
-    if ((y_dtype == BSG_E4M3) != (scale != nullptr)) return fail(BSG_ERR_NULLPTR, "scale goes with E4M3 codes");
+    // (a tensor without elements has no address)
+    if ((prob && tokens && !weight) || (weight && m && !prob))
+        return fail(BSG_ERR_NULLPTR, "weight and prob are given together or not at all");
+    if (y_dtype == BSG_E4M3 ? m && !scale : scale != nullptr) return fail(BSG_ERR_NULLPTR, "scale goes with E4M3 codes");
     if (m && (!y || (tokens && (!x || !row_of)) || (zero_pad && (!padded_offsets || !expert_rows))))
         return fail(BSG_ERR_NULLPTR, "x, row_of and y are required, padded_offsets and expert_rows with zero_pad");
     if (!aligned16(x) || !aligned16(y)) return fail(BSG_ERR_ALIGN, "x and y must be 16-byte aligned");
@@ -150,8 +152,9 @@ int bsg_validate_moe_gather_bwd(const void *dy, const float *dprob, const int32_
     if (int r = check_rows(m)) return r;
     if (int r = check_float(dtype, "dtype")) return r;
     if (int r = check_hidden(hidden, 16 / elem_bytes(dtype))) return r;
-    if (!dweight != !dprob) return fail(BSG_ERR_NULLPTR, "dprob and dweight are given together or not at all");
-    if (!dx && !dweight) return fail(BSG_ERR_NULLPTR, "dx or dweight is required");
+    if ((dprob && tokens && !dweight) || (dweight && m && !dprob))
+        return fail(BSG_ERR_NULLPTR, "dprob and dweight are given together or not at all");
+    if (tokens && !dx && !dweight) return fail(BSG_ERR_NULLPTR, "dx or dweight is required");
     if (tokens && (!row_of || (dx && m && !dy))) return fail(BSG_ERR_NULLPTR, "row_of is required, and dy for dx");
     if (!aligned16(dy) || !aligned16(dx)) return fail(BSG_ERR_ALIGN, "dy and dx must be 16-byte aligned");
     if (!aligned4(row_of) || !aligned4(dprob) || !aligned4(dweight))
@@ -201,7 +204,7 @@ int bsg_validate_moe_combine_bwd(const void *dout, const void *y, const int32_t 
     if (int r = check_rows(m)) return r;
     if (int r = check_float(dtype, "dtype")) return r;
     if (int r = check_hidden(hidden, 16 / elem_bytes(dtype))) return r;
-    if (!dy && !dweight) return fail(BSG_ERR_NULLPTR, "dy or dweight is required");
+    if (tokens && m && !dy && !dweight) return fail(BSG_ERR_NULLPTR, "dy or dweight is required");
     if (tokens && (!dout || !row_of || (dweight && m && !y)))
         return fail(BSG_ERR_NULLPTR, "dout and row_of are required, and y for dweight");
     if (dy && zero_pad && m && (!padded_offsets || !expert_rows))

@@ -531,7 +531,8 @@ int bsg_validate_gemm_glu_bwd(const void *dh, const void *x, const void *w_gate,
  * multiple of 256 up to 2^30, 1 <= hidden <= 2^20; rows are whole 16-byte
  * pieces (ALIGN otherwise).  Sums are held in fp32 and rounded once.
  * The products and quant_fp8 take rows up to 2^22, N and K up to 2^20
- * (UNSUPPORTED past that).
+ * (UNSUPPORTED past that).  A tensor without elements (no tokens, m = 0) may
+ * be NULL, also beside one that it is given together with.
  * ------------------------------------------------------------------------- */
 
 /* Rows that any routing of these sizes fits in: floor((P + 255 min(L, P)) /
