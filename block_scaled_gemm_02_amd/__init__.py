@@ -98,6 +98,8 @@ def lib():
         L.bsg_moe_rows.argtypes = [i64] * 3
         L.bsg_plan_string.restype = ctypes.c_char_p
         L.bsg_plan_string.argtypes = [i32, i64, i64, i64]
+        L.bsg_grouped_plan_string.restype = ctypes.c_char_p
+        L.bsg_grouped_plan_string.argtypes = [i32] + [i64] * 5 + [i32]
         L.bsg_status_string.restype = ctypes.c_char_p
         L.bsg_status_string.argtypes = [i32]
         L.bsg_last_error.restype = ctypes.c_char_p
@@ -117,7 +119,7 @@ def symbols():
             "bsg_validate_grouped_gemm_discrete", "bsg_validate_grouped_gemm_srelu_discrete",
             "bsg_check_padded_offsets", "bsg_status_string", "bsg_last_error", "bsg_version",
             *_FFN_OPS, *("bsg_validate_" + n for n in _FFN_OPS), "bsg_workspace_bytes",
-            "bsg_plan_string", *_MOE_OPS, *("bsg_validate_" + n for n in _MOE_OPS), "bsg_moe_rows"]
+            "bsg_plan_string", "bsg_grouped_plan_string", *_MOE_OPS, *("bsg_validate_" + n for n in _MOE_OPS), "bsg_moe_rows"]
 
 
 def _ptr(t):
@@ -465,12 +467,15 @@ def _refuse_sizes(*sizes):
     raise BsgError(2 if min(sizes) < 0 else 5, lib().bsg_last_error().decode())
 
 
-def plan_string(name, m, n, k) -> str:
+def plan_string(name, m, n, k, num_experts=1, max_rows=0, expert_rows=True) -> str:
     """How operator `name` goes out at these sizes (see include/bsg.h): for
-    tests and tuning."""
-    if name not in _WS_OPS or name == "moe_sort":
+    tests and tuning.  The last three count for the grouped products alone."""
+    if name in ("grouped_gemm_fp8", "grouped_gemm_fp8_wgrad"):
+        s = lib().bsg_grouped_plan_string(int(name.endswith("wgrad")), m, n, k, num_experts, max_rows, int(bool(expert_rows)))
+    elif name not in _WS_OPS or name == "moe_sort":
         raise ValueError(f"no product named {name!r}")
-    s = lib().bsg_plan_string(_WS_OPS[name], m, n, k)
+    else:
+        s = lib().bsg_plan_string(_WS_OPS[name], m, n, k)
     if s is None:
         _refuse_sizes(m, n, k)
     return s.decode()

@@ -587,11 +587,7 @@ const char *bsg_plan_string(int op, int64_t m, int64_t n, int64_t k)
         else return "none";
     } else if (op == BSG_OP_GEMM_FP8) {
         if (!m || !n) return "none";
-        const bsg::moe::Plan p = bsg::moe::plan_gemm_fp8(m, n, k);
-        static const char *const shape[3] = {"Big", "Mid", "Small"};
-        if (p.few) snprintf(text, sizeof text, "few %d", p.few);
-        else if (p.splits > 1) snprintf(text, sizeof text, "%s / %d", shape[p.shape], p.splits);
-        else snprintf(text, sizeof text, "%s", shape[p.shape]);
+        bsg::moe::text_of(bsg::moe::plan_gemm_fp8(m, n, k), text, sizeof text);
     } else {
         fail(BSG_ERR_SHAPE, "op %d is not a product", op);
         return nullptr;

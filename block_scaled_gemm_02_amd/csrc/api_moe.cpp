@@ -2,6 +2,7 @@
 // rules of api.cpp.
 #include "api.hpp"
 #include "moe/moe.hpp"
+#include "moe/plan.hpp"
 
 using namespace bsg::api;
 
@@ -310,6 +311,22 @@ int grouped_gemm_fp8(const uint8_t *a, const uint8_t *b, const float *a_scale, c
     const bsg::moe::Fp8Args args{a, b, a_scale, b_scale, padded_offsets, expert_rows, c, nullptr, m, n, k, (int)num_experts,
                                  (int)(max_rows < m ? max_rows : m), bsg::moe::GROUP_ROWS, a_dtype, c_dtype};
     return launch_status(bsg::moe::launch_fp8(args, static_cast<hipStream_t>(stream)), "grouped_gemm_fp8");
+}
+
+const char *bsg_grouped_plan_string(int wgrad, int64_t m, int64_t n, int64_t k, int64_t num_experts, int64_t max_rows,
+                                    int expert_rows)
+{
+    static thread_local char text[64];
+    if (check_ffn_sizes(m, n, k) || check_experts(num_experts) || check_rows(m)) return nullptr;
+    if (max_rows < 0) {
+        fail(BSG_ERR_SHAPE, "max_rows=%lld must not be negative", (long long)max_rows);
+        return nullptr;
+    }
+    if (!n || (wgrad ? !k : !m)) return "none";
+    bsg::moe::text_of(wgrad ? bsg::moe::plan_wgrad_fp8(m, n, k, num_experts)
+                            : bsg::moe::plan_grouped_fp8(m, n, k, num_experts, max_rows < m ? max_rows : m, expert_rows != 0),
+                      text, sizeof text);
+    return text;
 }
 
 int bsg_validate_grouped_gemm_fp8_wgrad(const uint8_t *a, const uint8_t *b, const float *a_scale, const float *b_scale,

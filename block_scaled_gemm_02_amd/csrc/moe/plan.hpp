@@ -1,6 +1,8 @@
 // How a product of 8-bit floats goes out: host code, shared by the launches,
 // the workspace size and the plan string.
 #pragma once
+#include <cstdio>
+
 #include "../ffn/plan.hpp"
 
 namespace bsg {
@@ -112,6 +114,14 @@ inline Plan plan_wgrad_fp8(int64_t m, int64_t n, int64_t k, int64_t num_experts)
 {
     const Plan big = plan_with(BIG, 1, n, k, m / num_experts, num_experts), mid = plan_with(MID, 1, n, k, m / num_experts, num_experts);
     return mid.us < big.us ? mid : big;
+}
+
+inline void text_of(const Plan &p, char *text, size_t size)
+{
+    static const char *const shape[3] = {"Big", "Mid", "Small"};
+    if (p.few) snprintf(text, size, "few %d", p.few);
+    else if (p.splits > 1) snprintf(text, size, "%s / %d", shape[p.shape], p.splits);
+    else snprintf(text, size, "%s", shape[p.shape]);
 }
 
 }  // namespace moe

@@ -427,6 +427,11 @@ int64_t bsg_workspace_bytes(int op, int64_t m, int64_t n, int64_t k);
  * part of the interface. */
 const char *bsg_plan_string(int op, int64_t m, int64_t n, int64_t k);
 
+/* The same of grouped_gemm_fp8, called with expert_rows or without, and, with
+ * wgrad set, of grouped_gemm_fp8_wgrad (which takes no max_rows or expert_rows). */
+const char *bsg_grouped_plan_string(int wgrad, int64_t m, int64_t n, int64_t k, int64_t num_experts,
+                                    int64_t max_rows, int expert_rows);
+
 /*
  * quant_i8 -- rows to symmetric 8-bit integers, one scale a row:
  *     t = max(max_k |x[m,k]|, 2^-100)
