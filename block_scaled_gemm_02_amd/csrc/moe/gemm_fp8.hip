@@ -4,9 +4,12 @@
 //   C[m, n] = sum_kb  a_scale[kb, m] b_scale[n / 128, kb]  sum_{k in kb} a[m, k] b[n, k]
 //
 // C is fp16 or bf16: the matrix instruction (both of the card's 8-bit ones) drops
-// of each 8 products the bits below 2^-13 of the largest, 5e-5 of the result on
-// random operands, below those types' rounding.  A block's sum, its factor and
-// the sum over blocks are fp32; C is rounded once.
+// of each 8 products the bits below 2^-13 of the largest, towards zero.  That is
+// less than 7 * 2^-13 = 8.5e-4 of the sum of magnitudes, at worst more than an
+// fp16 rounding, and 5e-5 of the result on random normal operands: the error of
+// C against 64 bits is then 1.6615e-3 in bf16 and 2.082e-4 in fp16, that of the
+// exact sum rounded 1.6614e-3 and 2.077e-4.  A block's sum, its factor and the
+// sum over blocks are fp32; C is rounded once.
 //
 // Tiles (fp8_tile.hpp) or a kernel for few rows, by plan.hpp.  Measured: 8192^3
 // 407-430 us; 32768 unevenly routed rows, 32 experts of 4096 x 7168, 855-920 us (12%
