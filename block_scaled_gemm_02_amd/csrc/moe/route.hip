@@ -23,17 +23,17 @@ __device__ __forceinline__ int row_at(const int32_t *row_of, int64_t pair, int64
     return (uint64_t)(uint32_t)r < (uint64_t)m ? r : -1;
 }
 
-// Rows of an expert that hold no pair, a quarter of the most there can be for
-// each workgroup that is added for them.
+// Rows of an expert that hold no pair, up to 255 behind moe_sort: four workgroups
+// are added for them, which take 64 rows each in turn.
 struct Pad {
     int64_t first, last;
+    __device__ __forceinline__ int64_t row(int64_t i) const { return first + 256 * (i >> 6) + (i & 63); }
 };
 __device__ __forceinline__ Pad pad_of(int b, const int32_t *padded_offsets, const int32_t *expert_rows, int64_t m)
 {
     const int e = b / 4, q = b % 4;
     const int64_t begin = e ? padded_offsets[e - 1] : 0, end = min((int64_t)padded_offsets[e], m);
-    const int64_t first = begin + expert_rows[e] + 64 * q;
-    return {max((int64_t)0, first), min(end, first + 64)};
+    return {max((int64_t)0, begin + expert_rows[e] + 64 * q), end};
 }
 
 // Copies 16-byte pieces of rows.
@@ -44,7 +44,7 @@ __global__ __launch_bounds__(256) void k_gather(GatherArgs p, int lg, unsigned r
     u32x4 *const y = (u32x4 *)p.y;
     if (blockIdx.x >= rows_grid) {
         const Pad d = pad_of(blockIdx.x - rows_grid, p.padded_offsets, p.expert_rows, p.m);
-        for (int64_t r = d.first + sub; r < d.last; r += per) {
+        for (int64_t i = sub, r; (r = d.row(i)) < d.last; i += per) {
             if (col < pieces) y[r * pieces + col] = u32x4{0, 0, 0, 0};
             if (col == 0 && p.prob) p.prob[r] = 0.0f;
         }
@@ -73,7 +73,7 @@ __global__ __launch_bounds__(256) void k_gather_fp8(GatherArgs p, int lg, unsign
     if (blockIdx.x >= rows_grid) {
         const Pad d = pad_of(blockIdx.x - rows_grid, p.padded_offsets, p.expert_rows, p.m);
         const float least = scale_of<false>(0).scale;
-        for (int64_t r = d.first + sub; r < d.last; r += per) {
+        for (int64_t i = sub, r; (r = d.row(i)) < d.last; i += per) {
             if (col < pieces) y[r * pieces + col] = u32x2{0, 0};
             if (first) sc[r] = least;
             if (col == 0 && p.prob) p.prob[r] = 0.0f;
@@ -153,7 +153,7 @@ __global__ __launch_bounds__(256) void k_combine_bwd(CombineBwdArgs p, int lg, u
     u32x4 *const dy = (u32x4 *)p.dy;
     if (blockIdx.x >= rows_grid) {
         const Pad d = pad_of(blockIdx.x - rows_grid, p.padded_offsets, p.expert_rows, p.m);
-        for (int64_t r = d.first + sub; r < d.last; r += per)
+        for (int64_t i = sub, r; (r = d.row(i)) < d.last; i += per)
             for (int64_t c = c0; c < pieces; c += tpr) dy[r * pieces + c] = u32x4{0, 0, 0, 0};
         return;
     }

@@ -527,8 +527,9 @@ int bsg_validate_gemm_glu_bwd(const void *dh, const void *x, const void *w_gate,
  * Row order.  A pair is a token and one of its top_k choices, p = token * top_k
  * + choice.  Sorted rows are as the grouped calls take them: expert e's pairs
  * are the rows from padded_offsets[e-1] (0 for e = 0) on, expert_rows[e] of
- * them, in the order of the pairs, and the range is rounded up to a multiple
- * of 256 with rows that hold no pair.  row_of (tokens, top_k) says which row a
+ * them, in the order of the pairs, and the range goes on with rows that hold no
+ * pair: up to the next multiple of 256 behind moe_sort, up to any later one where
+ * a program lays out its own.  row_of (tokens, top_k) says which row a
  * pair has; a value outside [0, m) says that it has none.  No two pairs share a
  * row.  The rows behind the last expert are neither read nor written, except
  * that moe_sort writes all m of pair_of.
@@ -565,9 +566,10 @@ int moe_sort(const int32_t *expert, int32_t *padded_offsets, int32_t *expert_row
  *   E4M3 codes with scale (ceil(hidden/128), m) fp32, as quant_fp8 makes them
  *   (hidden a multiple of 16; scale NULL otherwise).  weight (tokens, top_k)
  *   and prob (m,) fp32: both or neither; prob is what the grouped calls take.
- *   zero_pad: the rows of an expert's range that hold no pair become zeros (the
- *   scale of zeros, prob 0); without it they stay as they are, which
- *   grouped_gemm_fp8 with expert_rows allows.
+ *   zero_pad: the rows of an expert's range behind its expert_rows become zeros
+ *   (the scale of zeros, prob 0); without it they stay as they are, which
+ *   grouped_gemm_fp8 with expert_rows allows.  Rows that no pair names (one taken
+ *   out of row_of after the sort) stay as they are in either case.
  */
 int moe_gather(const void *x, const int32_t *row_of, const int32_t *padded_offsets,
                const int32_t *expert_rows, const float *weight, void *y, float *scale, float *prob,
