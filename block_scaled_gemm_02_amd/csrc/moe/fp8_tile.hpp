@@ -39,8 +39,8 @@
 // a block, at its beginning (25.6 us for 23.5 at 56 blocks).
 //
 // A workgroup's tiles follow each other in the ring.  What bounds the largest
-// one: with all compute units at work the power limit; 8192^3 takes 407-425 us by
-// card, 2590-2700 TFLOP/s, the matrix cores 67% busy at the clock that is left (on
+// one: with all compute units at work the power limit; 8192^3 takes 424-449 us by
+// card, 2450-2590 TFLOP/s, the matrix cores 67% busy at the clock that is left (on
 // zeros 320 us; without the multiply-adds 9% less).  Each tile's way out costs 5
 // us, 128 KB of C a compute unit.
 #pragma once

@@ -11,12 +11,12 @@
 // exact sum rounded 1.6614e-3 and 2.077e-4.  A block's sum, its factor and the
 // sum over blocks are fp32; C is rounded once.
 //
-// Tiles (fp8_tile.hpp) or a kernel for few rows, by plan.hpp.  Measured: 8192^3
-// 407-430 us; 32768 unevenly routed rows, 32 experts of 4096 x 7168, 855-920 us (12%
-// more rows than pairs by the padding, in 8.9 rounds of tiles); their gradient of 32 x
-// 4096 x 2048 from 16382 rows 189 us, 236 from HBM (0.69 GB); 32 tokens through 64
-// experts of 4096 x 7168 304 us (1.75 GB, 5.8 TB/s); 1 x 7168 x 2048 4.3 us, 5.0
-// from HBM.
+// Tiles (fp8_tile.hpp) or a kernel for few rows, by plan.hpp.  Measured, calls in a
+// row by card: 8192^3 424-449 us; 32768 unevenly routed rows, 32 experts of 4096 x
+// 7168, 865-930 us (12% more rows than pairs by the padding, in 8.9 rounds of tiles);
+// their gradient of 32 x 4096 x 2048 from 16382 rows 197 us, 247 from HBM (0.69
+// GB); 32 tokens through 64 experts of 4096 x 7168 301 us (1.73 GB, 5.8 TB/s); 1 x
+// 7168 x 2048 4.3 us, 5.0 from HBM.
 #include "../ffn/few.hpp"
 #include "fp8_tile.hpp"
 #include "plan.hpp"

@@ -7,8 +7,8 @@
 // 4 waves, and the transposed codes are formed 8 rows at a time and turned
 // round in the LDS.
 // Bound by memory: 16384 x 4096 bf16 both ways (272 MB) takes 58 us, 4.7 TB/s (a
-// large copy reaches 4.5-4.7), 51 us with the input in the memory-side cache; 32
-// matrices of 2048 x 4096 fp32 in tiles, both ways (1.61 GB), 301 us, 5.4 TB/s.
+// plain copy reaches 5.4), 47 us with the input in the memory-side cache; 32
+// matrices of 2048 x 4096 fp32 in tiles, both ways (1.61 GB), 293 us, 5.5 TB/s.
 #include "rows.hpp"
 
 namespace bsg {

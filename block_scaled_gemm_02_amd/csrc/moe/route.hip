@@ -8,8 +8,9 @@
 // write it once): memory bounds them.  4001 tokens of 7168 bf16 to E4M3 rows, 8
 // each (270 MB) 57 us with the sort, 46 us without it; 8192 of 4096 bf16 to 8 rows
 // each, padding zeroed (640 MB) 113 us; their gradients back (604 MB) 116 us, 5.2
-// TB/s; moe_combine's gradients (1.21 GB) 232 us, 5.2 TB/s (a large copy reaches
-// 4.5-4.7).  Few tokens are bound by the launch: 33 of 7168 fp16 4.7 us.
+// TB/s; moe_combine's gradients (1.21 GB) 232 us, 5.2 TB/s (a plain copy reaches
+// 5.4, reads alone 6.9, stores alone 5.8).  Few tokens are bound by the launch: 33 of
+// 7168 fp16 4.7 us.
 #include "rows.hpp"
 
 namespace bsg {
