@@ -96,10 +96,10 @@ def _targets(body, i):
         return ([] if op == "s_branch" else [i + 1]) + [_index(body, to)]
     if op == "s_setpc_b64":
         # a far jump: s_getpc, s_add_u32, s_addc_u32 with the distance
-        (start, get, _), (_, add, low), (_, addc, _) = body[i - 3:i]
-        if (get, add, addc) != ("s_getpc_b64", "s_add_u32", "s_addc_u32"):
+        before = body[max(0, i - 3):i]
+        if [b[1] for b in before] != ["s_getpc_b64", "s_add_u32", "s_addc_u32"]:
             raise RuntimeError(f"a jump to an unknown place at {at:#x}")
-        step = int(low.split(",")[2], 0) & 0xFFFFFFFF
+        start, step = before[0][0], int(before[1][2].split(",")[2], 0) & 0xFFFFFFFF
         return [_index(body, start + 4 + (step - (1 << 32) if step >= 1 << 31 else step))]
     if op.startswith(("s_swappc", "s_call")):
         raise RuntimeError(f"a call at {at:#x}")

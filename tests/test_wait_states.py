@@ -69,6 +69,8 @@ def test_far_jumps_are_followed():
     with pytest.raises(RuntimeError):
         found(FILL, FILL, FILL, FILL, ("s_setpc_b64", "s[10:11]"), END)
     with pytest.raises(RuntimeError):
+        found(("s_setpc_b64", "s[10:11]"), END)
+    with pytest.raises(RuntimeError):
         found(("s_swappc_b64", "s[0:1], s[2:3]"), END)
 
 
